@@ -18,6 +18,16 @@
  * gradients) and veda_tile_sparse_attn_backward_grid (dQ, dK, dV of the
  * grid-order attention over the same selected tiles).
  *
+ * The rest of a transformer layer's attention block stands on both sides of
+ * that path:
+ *
+ *   veda_add_rms_norm_fp8 (residual + norm, e4m3)  ->  veda_gemm_fp8 (QKV product)
+ *   ->  veda_qkv_norm_rope (Q/K norm, rotary positions, grid order)  ->  attention
+ *   ->  veda_quant_fp8 (token order, e4m3)  ->  veda_gemm_fp8 (output product)
+ *
+ * with veda_add_rms_norm(_backward) and veda_qkv_norm_rope_backward for
+ * training.
+ *
  * Conventions shared by every call
  * --------------------------------
  * Layout.  Grid-order tensors are [B, heads, N, d] row-major bf16 with
@@ -341,6 +351,158 @@ veda_status veda_tile_sparse_attn_backward_grid(const veda_problem* p, const voi
                                                 const int32_t* idx, int32_t k_max, float scale, void* dq,
                                                 void* dk, void* dv, void* workspace, size_t workspace_bytes,
                                                 void* stream);
+
+/* ---------------------------------------------------------------- around the attention: residual and norm */
+
+/* Element types of the operators around the attention. */
+typedef enum { VEDA_BF16 = 0, VEDA_FP16 = 1, VEDA_FP32 = 2 } veda_dtype;
+
+/* Residual addition and RMS norm of `rows` rows of C channels:
+ *   h = x + delta, rounded to x's type;   y = h * (mean_c h^2 + eps)^(-1/2) * weight
+ * (the norm is taken of the rounded h, which is what the backward call reads).
+ * x [rows, C] (row stride ldx elements) and h are of x_type, the residual
+ * stream's; delta [rows, C] (row stride ldd) and y of delta_type, the
+ * sublayers'.  The two types are equal, or VEDA_FP32 and VEDA_BF16.  delta may
+ * be NULL (then h = x); h may be NULL, and may be x itself if ldx == C.
+ * weight [C] fp32.  rstd [rows] fp32 or NULL: the factor above, for the backward
+ * call.  h and y are dense [rows, C].  C a multiple of 8 in [8, 16384]; ldx and
+ * ldd multiples of 8, at least C; rows >= 0; eps >= 0. */
+veda_status veda_add_rms_norm(int64_t rows, int32_t C, veda_dtype x_type, const void* x, int64_t ldx,
+                              veda_dtype delta_type, const void* delta, int64_t ldd, const float* weight, float eps,
+                              void* h, void* y, float* rstd, void* stream);
+
+/* The same with y in 8 bits: y8 [rows, C] e4m3, y_scale [ceil(C/128), rows]
+ * fp32.  Per row and block of 128 channels, with a the block's largest |y| or
+ * 2^-100 if that is larger: y_scale = a / 448, y8 = e4m3(y * (448 / a)),
+ * nearest even; the block stands for y8 * y_scale.  A block that holds an
+ * infinity or NaN stands for NaN.  This is the inference form: it has no
+ * backward. */
+veda_status veda_add_rms_norm_fp8(int64_t rows, int32_t C, veda_dtype x_type, const void* x, int64_t ldx,
+                                  veda_dtype delta_type, const void* delta, int64_t ldd, const float* weight,
+                                  float eps, void* h, void* y8, float* y_scale, void* stream);
+
+/* Workspace bytes veda_add_rms_norm_backward needs for dweight (on the current
+ * device: it depends on the number of SMs). */
+veda_status veda_add_rms_norm_backward_workspace(int64_t rows, int32_t C, size_t* bytes);
+
+/* Gradients of veda_add_rms_norm.  h and rstd as the forward wrote them; dy
+ * [rows, C] of delta_type and dh [rows, C] of x_type (or NULL: zero), the
+ * upstream gradients of y and of h.  With g = dy * weight:
+ *   d = dh + rstd (g - h mean_c(g h) rstd^2),   dweight = sum_rows dy h rstd.
+ * dx is d in x_type, ddelta the same in delta_type; either may be NULL, and
+ * dx may be dh.  dweight [C] fp32 (written in full) or NULL.  All tensors
+ * dense.  workspace: device scratch of veda_add_rms_norm_backward_workspace
+ * bytes, 16-byte aligned; needed (non-NULL) only for dweight.  Sums run in a
+ * fixed order without atomics: a rerun on the same device gives the same
+ * bits. */
+veda_status veda_add_rms_norm_backward(int64_t rows, int32_t C, veda_dtype x_type, const void* h,
+                                       veda_dtype delta_type, const void* dy, const void* dh, const float* weight,
+                                       const float* rstd, void* dx, void* ddelta, float* dweight, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------- around the attention: 8-bit product */
+
+/* Activations to e4m3 by the rule of veda_add_rms_norm_fp8.  x holds element
+ * (b, n, h, c) at x[b * stride_b + n * stride_n + h * stride_h + c], b < B,
+ * n < N, h < heads, c < d; q [B*N, heads*d] e4m3 and scale
+ * [ceil(heads*d/128), B*N] fp32 hold row b*N + n and column h*d + c.  So rows
+ * [R, C] are B = 1, N = R, heads = 1, d = C, and the attention's grid-order
+ * output [B, heads, N, d] comes out in the row order of the output product.
+ * d and the strides are multiples of 8 (elements), strides >= 0. */
+veda_status veda_quant_fp8(int32_t B, int64_t N, int32_t heads, int32_t d, veda_dtype type, const void* x,
+                           int64_t stride_b, int64_t stride_n, int64_t stride_h, void* q, float* scale, void* stream);
+
+/* Weights to e4m3 by the same rule with one scale per 128 x 128 block:
+ * w [N, K] dense of `type`, q [N, K] e4m3, scale [ceil(N/128), ceil(K/128)]
+ * fp32.  K a multiple of 8. */
+veda_status veda_quant_fp8_weight(int32_t N, int32_t K, veda_dtype type, const void* w, void* q, float* scale,
+                                  void* stream);
+
+/* C = A B^T in 8 bits with a scale for each block of 128:
+ *   out[m, n] = sum_kb a_scale[kb, m] b_scale[n / 128, kb] sum_{k in block kb} A[m, k] B[n, k]  (+ bias[n])
+ * a [M, K] e4m3 (row stride lda bytes), a_scale [ceil(K/128), M] fp32;
+ * b [N, K] e4m3 (row stride ldb bytes, a linear layer's weight as it is
+ * stored), b_scale [ceil(N/128), ceil(K/128)] fp32; bias [N] fp32 or NULL; out
+ * [M, N] (row stride ldo elements) of out_type VEDA_BF16 or VEDA_FP32.
+ * K, lda and ldb multiples of 16; N and ldo multiples of 8; M >= 0.  Runs on
+ * the tcgen05 tensor cores with fp32 accumulation inside a block and fp32 sums
+ * over blocks; deterministic.  Inference only: no backward. */
+veda_status veda_gemm_fp8(int32_t M, int32_t N, int32_t K, const void* a, int64_t lda, const float* a_scale,
+                          const void* b, int64_t ldb, const float* b_scale, const float* bias, veda_dtype out_type,
+                          void* out, int64_t ldo, void* stream);
+
+/* ---------------------------------------------------------------- around the attention: rotary positions */
+
+/* Norm of Q and K ahead of the rotation: none, over all heads of a token
+ * (weights [heads*d]), or over each head (weights [d], shared by the heads). */
+typedef enum { VEDA_NORM_NONE = 0, VEDA_NORM_ROW = 1, VEDA_NORM_HEAD = 2 } veda_norm;
+
+/* The two channels of a rotated pair: neighbours (2i, 2i + 1), or the halves
+ * (i, i + dim/2) of their axis's channels. */
+typedef enum { VEDA_PAIR_INTERLEAVED = 0, VEDA_PAIR_HALVES = 1 } veda_pairing;
+
+/* Rotary positions over a token grid.  The first dim_t channels of each head
+ * are turned by the token's time index, the next dim_h by its height index and
+ * the next dim_w by its width index (each even, their sum at most d); the rest
+ * are not turned.  table_t / _h / _w: DEVICE fp32 (cos, sin) of each index and
+ * pair, [grid.T, dim_t/2, 2], [grid.H, dim_h/2, 2] and [grid.W, dim_w/2, 2]
+ * (veda_rope_table writes one; a table that starts at a later row moves the
+ * grid along that axis); NULL where the axis has no channels. */
+typedef struct {
+  int32_t B, heads, d;          /* d in {64, 128}, heads in [1, VEDA_MAX_HEADS] */
+  veda_grid grid;
+  int32_t dim_t, dim_h, dim_w;
+  const float* table_t;
+  const float* table_h;
+  const float* table_w;
+  veda_pairing pairing;
+  veda_norm norm;
+  float eps;
+} veda_rope;
+
+/* A token-order tensor: element (b, n, h, c) at x[b * stride_b + n * stride_n +
+ * h * stride_h + c].  Strides in elements, multiples of 8, >= 0.  A packed
+ * [B, N, 3, heads, d] product is three of these with the same strides. */
+typedef struct {
+  void* x;
+  int64_t stride_b, stride_n, stride_h;
+} veda_tokens;
+
+/* (cos, sin) of (start + step * i) * theta^(-2 j / dim) for i < n, j < dim/2, into
+ * table [n, dim/2, 2] DEVICE fp32.  Angles are computed in fp64.  dim even in
+ * [2, 128], theta > 0, n >= 0. */
+veda_status veda_rope_table(int32_t n, int32_t dim, double theta, double start, double step, float* table,
+                            void* stream);
+
+/* Norm of Q and K, their rotation, and the change to grid order in one pass:
+ * for each given operand, x of `type` in token order -> [B, heads, N, d] bf16,
+ *   q_out = R(q * rstd * wq),  k_out = R(k * rstd * wk),  v_out = v,
+ * rstd = (mean x^2 + eps)^(-1/2) over the norm's channels, and R turning the
+ * pair (a, b) into (a cos - b sin, a sin + b cos).  q, k and v may each be NULL
+ * together with their output (not all three).  wq, wk fp32, unused without a
+ * norm.  Outputs must not overlap inputs. */
+veda_status veda_qkv_norm_rope(const veda_rope* r, veda_dtype type, const veda_tokens* q, const veda_tokens* k,
+                               const veda_tokens* v, const float* wq, const float* wk, void* q_out, void* k_out,
+                               void* v_out, void* stream);
+
+/* Workspace bytes veda_qkv_norm_rope_backward needs (on the current device; 0
+ * without a norm). */
+veda_status veda_qkv_norm_rope_backward_workspace(const veda_rope* r, size_t* bytes);
+
+/* Gradients of veda_qkv_norm_rope: d_q, d_k, d_v [B, heads, N, d] bf16 (read)
+ * are the upstream gradients, q and k the forward's inputs (not read without
+ * a norm), dq, dk, dv token-order outputs of `type` with strides of their own
+ * (their rows must not overlap each other).  With g = R^T d_q:
+ *   dq = rstd (g wq - q mean(g wq q) rstd^2),   dwq = sum g q rstd,
+ * and the same for k; without a norm dq = g.  dv = d_v.  An operand whose
+ * upstream gradient is NULL is left out.  dwq, dwk fp32 shaped like the weights
+ * (written in full) or NULL.  workspace as for veda_add_rms_norm_backward;
+ * reruns give the same bits. */
+veda_status veda_qkv_norm_rope_backward(const veda_rope* r, veda_dtype type, const veda_tokens* q,
+                                        const veda_tokens* k, const float* wq, const float* wk, const void* d_q,
+                                        const void* d_k, const void* d_v, const veda_tokens* dq,
+                                        const veda_tokens* dk, const veda_tokens* dv, float* dwq, float* dwk,
+                                        void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------- status */
 

@@ -1,0 +1,249 @@
+"""CPU checks of the operators around the attention: refusals of the C entry
+points and of the torch functions (no call here launches a kernel), and the
+oracle's gradients against differences."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import layer_oracle as L
+
+PTR = 1 << 20       # stands for a 16-byte aligned device address; no refused call reads it
+
+
+@pytest.fixture(scope="module")
+def V():
+    import tile_sparse_attention_head_b200 as V
+    return V
+
+
+BF16, FP16, FP32 = 0, 1, 2
+INVALID, UNSUPPORTED = 1, 2
+
+
+def norm_args(**kw):
+    a = dict(rows=4, C=64, xt=BF16, x=PTR, ldx=64, dt=BF16, delta=PTR, ldd=64, w=PTR, eps=1e-6, h=PTR, y=PTR, s=PTR)
+    a.update(kw)
+    return list(a.values()) + [None]
+
+
+@pytest.mark.parametrize("bad", [
+    dict(rows=-1), dict(C=0), dict(C=60), dict(C=16392, ldx=16392, ldd=16392), dict(xt=7), dict(dt=FP16),
+    dict(xt=FP32, dt=FP16), dict(xt=BF16, dt=FP32), dict(ldx=56), dict(ldx=68), dict(ldd=56), dict(eps=-1.0),
+    dict(eps=float("nan")), dict(eps=float("inf")), dict(x=None), dict(w=None), dict(y=None), dict(x=PTR + 8),
+    dict(delta=PTR + 2), dict(h=PTR + 4), dict(y=PTR + 4), dict(w=PTR + 4), dict(ldx=72, h=PTR)])
+def test_norm_refusals(V, bad):
+    for name in ("veda_add_rms_norm", "veda_add_rms_norm_fp8"):
+        assert getattr(V.LIB, name)(*norm_args(**bad)) != 0, bad
+        assert V.LIB.veda_last_error().decode()
+
+
+def test_norm_fp8_needs_a_scale(V):
+    assert V.LIB.veda_add_rms_norm_fp8(*norm_args(s=None)) != 0
+
+
+def test_no_rows_is_no_work(V):
+    assert V.LIB.veda_add_rms_norm(*norm_args(rows=0)) == 0
+    assert V.LIB.veda_add_rms_norm_fp8(*norm_args(rows=0)) == 0
+    assert V.LIB.veda_add_rms_norm_backward(0, 64, BF16, PTR, BF16, PTR, None, PTR, PTR, PTR, None, None, None, 0, None) == 0
+    assert V.LIB.veda_quant_fp8(1, 0, 2, 64, BF16, PTR, 0, 64, 64, PTR, PTR, None) == 0
+    assert V.LIB.veda_gemm_fp8(0, 64, 64, PTR, 64, PTR, PTR, 64, PTR, None, BF16, PTR, 64, None) == 0
+    assert V.LIB.veda_rope_table(0, 32, 1e4, 0.0, 1.0, PTR, None) == 0
+
+
+@pytest.mark.parametrize("bad", [
+    dict(h=None), dict(dy=None), dict(w=None), dict(rstd=None), dict(dx=None, dd=None, dw=None), dict(ws=None),
+    dict(wsb=0), dict(h=PTR + 8), dict(dw=PTR + 4), dict(ws=PTR + 8), dict(C=12), dict(xt=FP16)])
+def test_norm_backward_refusals(V, bad):
+    a = dict(rows=4, C=64, xt=BF16, h=PTR, dt=BF16, dy=PTR, dh=PTR, w=PTR, rstd=PTR, dx=PTR, dd=PTR, dw=PTR, ws=PTR,
+             wsb=16)
+    a.update(bad)
+    assert V.LIB.veda_add_rms_norm_backward(*a.values(), None) != 0
+
+
+@pytest.mark.parametrize("bad", [
+    dict(B=-1), dict(N=-1), dict(heads=0), dict(d=0), dict(d=12), dict(t=3), dict(sb=4), dict(sn=-8), dict(sh=12),
+    dict(x=None), dict(q=None), dict(s=None), dict(x=PTR + 8), dict(heads=1 << 18), dict(B=1 << 20, N=1 << 20)])
+def test_quant_refusals(V, bad):
+    a = dict(B=1, N=8, heads=2, d=64, t=BF16, x=PTR, sb=0, sn=64, sh=512, q=PTR, s=PTR)
+    a.update(bad)
+    assert V.LIB.veda_quant_fp8(*a.values(), None) != 0
+
+
+@pytest.mark.parametrize("bad", [dict(N=0), dict(K=0), dict(K=12), dict(t=5), dict(w=None), dict(q=PTR + 8), dict(s=None)])
+def test_quant_weight_refusals(V, bad):
+    a = dict(N=8, K=64, t=BF16, w=PTR, q=PTR, s=PTR)
+    a.update(bad)
+    assert V.LIB.veda_quant_fp8_weight(*a.values(), None) != 0
+
+
+@pytest.mark.parametrize("bad", [
+    dict(M=-1), dict(N=0), dict(N=12), dict(K=0), dict(K=24), dict(lda=48), dict(lda=72), dict(ldb=48), dict(ldo=56),
+    dict(ldo=68), dict(t=FP16), dict(a=None), dict(sa=None), dict(b=None), dict(sb=None), dict(out=None),
+    dict(a=PTR + 8), dict(bias=PTR + 4), dict(out=PTR + 8), dict(M=(1 << 30) + 1), dict(M=1 << 30, N=1 << 30, ldo=1 << 30)])
+def test_gemm_refusals(V, bad):
+    a = dict(M=8, N=64, K=64, a=PTR, lda=64, sa=PTR, b=PTR, ldb=64, sb=PTR, bias=PTR, t=BF16, out=PTR, ldo=64)
+    a.update(bad)
+    assert V.LIB.veda_gemm_fp8(*a.values(), None) != 0
+
+
+@pytest.mark.parametrize("bad", [dict(n=-1), dict(dim=0), dict(dim=3), dict(dim=130), dict(theta=0.0),
+                                 dict(theta=float("inf")), dict(start=float("nan")), dict(step=float("inf")),
+                                 dict(t=None), dict(t=PTR + 4)])
+def test_table_refusals(V, bad):
+    a = dict(n=4, dim=32, theta=1e4, start=0.0, step=1.0, t=PTR)
+    a.update(bad)
+    assert V.LIB.veda_rope_table(*a.values(), None) != 0
+
+
+def rope(V, **kw):
+    from tile_sparse_attention_head_b200.binding import veda_rope
+    from tile_sparse_attention_head_b200.binding import veda_grid
+    a = dict(B=1, heads=2, d=64, grid=veda_grid(2, 3, 4), dt=16, dh=24, dw=24, tt=PTR, th=PTR, tw=PTR, pairing=0, norm=1,
+             eps=1e-6)
+    a.update(kw)
+    return veda_rope(*a.values())
+
+
+@pytest.mark.parametrize("bad", [
+    dict(B=0), dict(heads=0), dict(heads=100000), dict(d=96), dict(dt=17), dict(dt=-2), dict(dt=32), dict(tt=None),
+    dict(th=PTR + 4), dict(pairing=2), dict(norm=3), dict(eps=-1.0)])
+def test_rope_refusals(V, bad):
+    from tile_sparse_attention_head_b200.binding import veda_tokens
+    t = veda_tokens(PTR, 0, 128, 64)
+    r = rope(V, **bad)
+    assert V.LIB.veda_qkv_norm_rope(ctypes.byref(r), BF16, ctypes.byref(t), None, None, PTR, None, PTR, None, None,
+                                    None) != 0
+    n = ctypes.c_size_t()
+    assert V.LIB.veda_qkv_norm_rope_backward_workspace(ctypes.byref(r), ctypes.byref(n)) != 0
+
+
+def test_rope_operand_refusals(V):
+    from tile_sparse_attention_head_b200.binding import veda_grid, veda_tokens
+    r = rope(V)
+    ok = veda_tokens(PTR, 0, 128, 64)
+    R = ctypes.byref
+
+    def fwd(q=ok, w=PTR, out=PTR, t=BF16, r=r):
+        return V.LIB.veda_qkv_norm_rope(R(r), t, None if q is None else R(q), None, None, w, None, out, None, None, None)
+
+    assert fwd(q=None, out=None) != 0                          # nothing to do
+    assert fwd(out=None) != 0 and fwd(q=None) != 0             # an operand without its output, and the reverse
+    assert fwd(w=None) != 0 and fwd(w=PTR + 4) != 0
+    assert fwd(t=9) != 0
+    assert fwd(out=PTR + 8) != 0
+    for bad in (veda_tokens(None, 0, 128, 64), veda_tokens(PTR + 8, 0, 128, 64), veda_tokens(PTR, 0, 132, 64),
+                veda_tokens(PTR, 0, -128, 64), veda_tokens(PTR, 4, 128, 64), veda_tokens(PTR, 0, 128, 12)):
+        assert fwd(q=bad) != 0
+    for g in (veda_grid(0, 3, 4), veda_grid(2, 3, -1), veda_grid(1 << 20, 1 << 20, 1)):
+        assert fwd(r=rope(V, grid=g)) != 0
+
+    def bwd(q=ok, d_q=PTR, dq=ok, w=PTR, dw=None, ws=None, wsb=0, r=r):
+        return V.LIB.veda_qkv_norm_rope_backward(R(r), BF16, None if q is None else R(q), None, w, None, d_q, None, None,
+                                                 None if dq is None else R(dq), None, None, dw, None, ws, wsb, None)
+
+    assert bwd(d_q=None, dq=None) != 0
+    assert bwd(dq=None) != 0 and bwd(d_q=None) != 0
+    assert bwd(q=None) != 0 and bwd(w=None) != 0               # the norm's backward reads both
+    assert bwd(d_q=PTR + 8) != 0
+    assert bwd(dw=PTR) != 0                                    # no workspace
+    assert bwd(dw=PTR, ws=PTR, wsb=16) != 0 and bwd(dw=PTR + 4, ws=PTR, wsb=1 << 30) != 0
+    assert bwd(dw=PTR, ws=PTR, wsb=1 << 30, r=rope(V, norm=0)) != 0     # no weight to have a gradient
+    assert bwd(dq=veda_tokens(PTR, 0, 0, 64)) != 0             # rows that would be written twice
+    assert bwd(dq=veda_tokens(PTR, 0, 128, 0)) != 0
+
+
+def test_host_tensors_and_shapes_are_refused(V):
+    x, w = torch.zeros(4, 64, dtype=torch.bfloat16), torch.ones(64)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        V.add_rms_norm(x, x, w)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        V.add_rms_norm_fp8(x, x, w)
+    with pytest.raises(ValueError, match="shape"):
+        V.add_rms_norm(x, x[:2], w)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        V.quant_fp8(x)
+    with pytest.raises(ValueError, match="heads"):
+        V.quant_fp8_heads(x)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        V.quant_fp8_weight(x)
+    a, s = torch.zeros(4, 64, dtype=torch.float8_e4m3fn), torch.ones(1, 4)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        V.gemm_fp8(a, s, a, s)
+    qkv = torch.zeros(1, 24, 3, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="needs wq and wk"):
+        V.qkv_norm_rope(qkv, (2, 3, 4), (None, None, None))
+    with pytest.raises(ValueError, match="no weights"):
+        V.qkv_norm_rope(qkv, (2, 3, 4), (None, None, None), w, w, norm="none")
+    with pytest.raises(ValueError, match="do not fill"):
+        V.qkv_norm_rope(qkv, (2, 3, 5), (None, None, None), norm="none")
+    with pytest.raises(ValueError, match="norm must be"):
+        V.qkv_norm_rope(qkv, (2, 3, 4), (None, None, None), w, w, norm="both")
+    with pytest.raises(ValueError, match="pairing must be"):
+        V.qkv_norm_rope(qkv, (2, 3, 4), (None, None, None), norm="none", pairing="odd")
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        V.qkv_norm_rope(qkv, (2, 3, 4), (None, None, None), norm="none")
+    with pytest.raises(ValueError, match="packed"):
+        V.qkv_norm_rope((qkv, qkv), (2, 3, 4), (None, None, None), norm="none")
+
+
+def test_eight_bit_forms_refuse_gradients(V):
+    x = torch.zeros(4, 64, requires_grad=True)
+    w = torch.ones(64)
+    a, s = torch.zeros(4, 64, dtype=torch.float8_e4m3fn), torch.ones(1, 4)
+    for call in (lambda: V.add_rms_norm_fp8(x, None, w), lambda: V.quant_fp8(x),
+                 lambda: V.quant_fp8_heads(x.view(1, 1, 4, 64)), lambda: V.gemm_fp8(a, s, a, s, bias=x[0])):
+        with pytest.raises(ValueError, match="no gradient"):
+            call()
+
+
+# ---------------------------------------------------------------- the oracle's gradients against differences
+
+def differences(f, x, step=1e-5):
+    g = np.zeros_like(x)
+    flat, out = x.reshape(-1), g.reshape(-1)
+    for i in range(flat.size):
+        keep = flat[i]
+        flat[i] = keep + step
+        up = f()
+        flat[i] = keep - step
+        down = f()
+        flat[i] = keep
+        out[i] = (up - down) / (2 * step)
+    return g
+
+
+def test_oracle_norm_gradient_against_differences():
+    rng = np.random.default_rng(0)
+    h, w = rng.standard_normal((3, 10)), 1 + 0.2 * rng.standard_normal(10)
+    dy, dh = rng.standard_normal((3, 10)), rng.standard_normal((3, 10))
+
+    def loss():
+        return float((L.rms_norm(h, w, 1e-3)[0] * dy).sum() + (h * dh).sum())
+
+    d, dw = L.rms_norm_backward(h, w, 1e-3, dy, dh)
+    # central differences: error step^2 times third derivatives (order 10) + 2^-52 * 50 / step
+    assert np.abs(differences(loss, h) - d).max() < 1e-7
+    assert np.abs(differences(loss, w) - dw).max() < 1e-7
+
+
+@pytest.mark.parametrize("norm", ["row", "head", "none"])
+@pytest.mark.parametrize("halves", [False, True])
+def test_oracle_rope_gradient_against_differences(norm, halves):
+    rng = np.random.default_rng(1)
+    grid, dims, heads, d = (2, 2, 2), (4, 2, 4), 2, 12
+    x = rng.standard_normal((1, 8, heads, d))
+    w = None if norm == "none" else 1 + 0.2 * rng.standard_normal(heads * d if norm == "row" else d)
+    tables = [L.rope_table(n, dim, 100.0, 0.5, 1.0) for n, dim in zip(grid, dims)]
+    dout = rng.standard_normal((1, heads, 8, d))
+
+    def loss():
+        return float((L.norm_rope(x, w, grid, dims, tables, norm, halves, 1e-3) * dout).sum())
+
+    dx, dw, mag, magw = L.norm_rope_backward(x, w, grid, dims, tables, norm, halves, 1e-3, dout)
+    assert np.abs(differences(loss, x) - dx).max() < 1e-7
+    assert np.all(np.abs(dx) <= mag * (1 + 1e-12))
+    if w is not None:
+        assert np.abs(differences(loss, w) - dw).max() < 1e-7
+        assert np.all(np.abs(dw) <= magw * (1 + 1e-12))

@@ -54,7 +54,22 @@ class veda_mlp_grad(ctypes.Structure):
     _fields_ = [("w1", ctypes.c_void_p), ("b1", ctypes.c_void_p), ("w2", ctypes.c_void_p), ("b2", ctypes.c_void_p)]
 
 
+class veda_rope(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("heads", ctypes.c_int32), ("d", ctypes.c_int32), ("grid", veda_grid),
+                ("dim_t", ctypes.c_int32), ("dim_h", ctypes.c_int32), ("dim_w", ctypes.c_int32),
+                ("table_t", ctypes.c_void_p), ("table_h", ctypes.c_void_p), ("table_w", ctypes.c_void_p),
+                ("pairing", ctypes.c_int), ("norm", ctypes.c_int), ("eps", ctypes.c_float)]
+
+
+class veda_tokens(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_n", ctypes.c_int64),
+                ("stride_h", ctypes.c_int64)]
+
+
 _P = ctypes.POINTER(veda_problem)
+_RP = ctypes.POINTER(veda_rope)
+_TP = ctypes.POINTER(veda_tokens)
+_I32, _I64, _F, _D, _SZ = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_double, ctypes.c_size_t
 _V = ctypes.c_void_p
 _I32P = ctypes.POINTER(ctypes.c_int32)
 _SIG = {
@@ -84,6 +99,17 @@ _SIG = {
     "veda_attn_backward_workspace": [_P, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)],
     "veda_tile_sparse_attn_backward_grid": [_P, _V, _V, _V, _V, _V, _V, _V, ctypes.c_int32, ctypes.c_float, _V, _V,
                                             _V, _V, ctypes.c_size_t, _V],
+    "veda_add_rms_norm": [_I64, _I32, _I32, _V, _I64, _I32, _V, _I64, _V, _F, _V, _V, _V, _V],
+    "veda_add_rms_norm_fp8": [_I64, _I32, _I32, _V, _I64, _I32, _V, _I64, _V, _F, _V, _V, _V, _V],
+    "veda_add_rms_norm_backward_workspace": [_I64, _I32, ctypes.POINTER(_SZ)],
+    "veda_add_rms_norm_backward": [_I64, _I32, _I32, _V, _I32, _V, _V, _V, _V, _V, _V, _V, _V, _SZ, _V],
+    "veda_quant_fp8": [_I32, _I64, _I32, _I32, _I32, _V, _I64, _I64, _I64, _V, _V, _V],
+    "veda_quant_fp8_weight": [_I32, _I32, _I32, _V, _V, _V, _V],
+    "veda_gemm_fp8": [_I32, _I32, _I32, _V, _I64, _V, _V, _I64, _V, _V, _I32, _V, _I64, _V],
+    "veda_rope_table": [_I32, _I32, _D, _D, _D, _V, _V],
+    "veda_qkv_norm_rope": [_RP, _I32, _TP, _TP, _TP, _V, _V, _V, _V, _V, _V],
+    "veda_qkv_norm_rope_backward_workspace": [_RP, ctypes.POINTER(_SZ)],
+    "veda_qkv_norm_rope_backward": [_RP, _I32, _TP, _TP, _V, _V, _V, _V, _V, _TP, _TP, _TP, _V, _V, _V, _SZ, _V],
     "veda_sync_status": [_V],
     "veda_set_wait_timeout_ns": [ctypes.c_uint64],
     "veda_selftest_wait_timeout": [ctypes.c_uint64, _V],
@@ -393,6 +419,266 @@ def veda_head_error(p: Problem, o: torch.Tensor, o_ref: torch.Tensor, err: torch
                                _ptr(ref_sq, "ref_sq", torch.float32, (p.heads,)), _ptr(workspace, "workspace"),
                                workspace.numel() * workspace.element_size(), _stream(stream)), "veda_head_error")
     return err, ref_sq
+
+
+# ---------------------------------------------------------------- around the attention
+#
+# These take tensors of any device: the call runs on its tensors' device (all on
+# one) and, without a `stream`, on that device's current stream.
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_NORMS = {"none": 0, "row": 1, "head": 2}
+_PAIRINGS = {"interleaved": 0, "halves": 1}
+FP8 = torch.float8_e4m3fn
+
+
+def _type(t: torch.Tensor, name: str) -> int:
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be bfloat16, float16 or float32 (got {t.dtype})")
+    return code
+
+
+def _rows(t: Optional[torch.Tensor], name: str, shape=None) -> Tuple[Optional[int], int]:
+    """Pointer and row stride of a [rows, C] tensor whose channels are contiguous."""
+    if t is None:
+        return None, 0
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [rows, C] with contiguous channels")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _call(func: str, tensors, stream, *args) -> None:
+    """Runs the library function on the device of `tensors` (None entries are skipped)."""
+    dev = None
+    for t in tensors:
+        if t is not None:
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise ValueError(f"{func}: tensors are on {dev} and {t.device}")
+    fn = getattr(LIB, func)
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)), func)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(stream)), func)
+
+
+def _on_device(dev: torch.device, fn):
+    """fn() with `dev` current (the workspace sizes depend on the device)."""
+    if dev.index == torch.cuda.current_device():
+        return fn()
+    with torch.cuda.device(dev):
+        return fn()
+
+
+def veda_add_rms_norm(x: torch.Tensor, delta: Optional[torch.Tensor], weight: torch.Tensor, eps: float,
+                      h: Optional[torch.Tensor], y: torch.Tensor, rstd: Optional[torch.Tensor] = None,
+                      stream=None) -> torch.Tensor:
+    """h = x + delta and its RMS norm y, [rows, C]; y is of delta's type (x's without a delta)."""
+    xp, ldx = _rows(x, "x")
+    dp, ldd = _rows(delta, "delta", x.shape)
+    rows, C = x.shape
+    td = _type(y if delta is None else delta, "y" if delta is None else "delta")
+    _call("veda_add_rms_norm", (x, delta, weight, h, y, rstd), stream, rows, C, _type(x, "x"), xp, ldx, td, dp, ldd,
+          _ptr(weight, "weight", torch.float32, (C,)), eps, _ptr(h, "h", x.dtype, x.shape),
+          _ptr(y, "y", y.dtype if delta is None else delta.dtype, x.shape), _ptr(rstd, "rstd", torch.float32, (rows,)))
+    return y
+
+
+def veda_add_rms_norm_fp8(x: torch.Tensor, delta: Optional[torch.Tensor], weight: torch.Tensor, eps: float,
+                          h: Optional[torch.Tensor], y8: torch.Tensor, y_scale: torch.Tensor,
+                          stream=None) -> torch.Tensor:
+    """veda_add_rms_norm with y in e4m3 and a scale per row and 128 channels, [ceil(C/128), rows]."""
+    xp, ldx = _rows(x, "x")
+    dp, ldd = _rows(delta, "delta", x.shape)
+    rows, C = x.shape
+    tx = _type(x, "x")
+    _call("veda_add_rms_norm_fp8", (x, delta, weight, h, y8, y_scale), stream, rows, C, tx, xp, ldx,
+          tx if delta is None else _type(delta, "delta"), dp, ldd, _ptr(weight, "weight", torch.float32, (C,)), eps,
+          _ptr(h, "h", x.dtype, x.shape), _ptr(y8, "y8", FP8, x.shape),
+          _ptr(y_scale, "y_scale", torch.float32, ((C + 127) // 128, rows)))
+    return y8
+
+
+def veda_add_rms_norm_backward_workspace(rows: int, C: int, device=None) -> int:
+    n = _SZ()
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    _on_device(dev, lambda: _check(LIB.veda_add_rms_norm_backward_workspace(rows, C, ctypes.byref(n)),
+                                   "veda_add_rms_norm_backward_workspace"))
+    return int(n.value)
+
+
+def veda_add_rms_norm_backward(h: torch.Tensor, dy: torch.Tensor, dh: Optional[torch.Tensor], weight: torch.Tensor,
+                               rstd: torch.Tensor, dx: Optional[torch.Tensor], ddelta: Optional[torch.Tensor],
+                               dweight: Optional[torch.Tensor], workspace: Optional[torch.Tensor],
+                               stream=None) -> None:
+    """Gradients of veda_add_rms_norm: dx in h's type, ddelta in dy's type, dweight fp32; None leaves one out."""
+    shape = h.shape
+    if h.dim() != 2:
+        raise ValueError("h must be [rows, C]")
+    rows, C = shape
+    _call("veda_add_rms_norm_backward", (h, dy, dh, weight, rstd, dx, ddelta, dweight, workspace), stream, rows, C,
+          _type(h, "h"), _ptr(h, "h"), _type(dy, "dy"), _ptr(dy, "dy", None, shape), _ptr(dh, "dh", h.dtype, shape),
+          _ptr(weight, "weight", torch.float32, (C,)), _ptr(rstd, "rstd", torch.float32, (rows,)),
+          _ptr(dx, "dx", h.dtype, shape), _ptr(ddelta, "ddelta", dy.dtype, shape),
+          _ptr(dweight, "dweight", torch.float32, (C,)), _ptr(workspace, "workspace"),
+          0 if workspace is None else workspace.numel() * workspace.element_size())
+
+
+def veda_quant_fp8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, stream=None) -> torch.Tensor:
+    """[rows, C], or the attention's grid-order [B, heads, N, d], to e4m3 rows [rows, C] (B*N rows of heads*d
+    channels) and scales [ceil(C/128), rows].  Channels contiguous, other strides free multiples of 8."""
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    if x.dim() == 2:
+        (N, d), (sn, sd) = x.shape, x.stride()
+        B, heads, sb, sh = 1, 1, 0, 0
+    elif x.dim() == 4:
+        (B, heads, N, d), (sb, sh, sn, sd) = x.shape, x.stride()
+    else:
+        raise ValueError("x must be [rows, C] or [B, heads, N, d]")
+    if d > 1 and sd != 1:
+        raise ValueError("the channels of x must be contiguous")
+    rows, C = B * N, heads * d
+    _call("veda_quant_fp8", (x, q, scale), stream, B, N, heads, d, _type(x, "x"), x.data_ptr(),
+          sb if B > 1 else 0, sn if N > 1 else 0, sh if heads > 1 else 0,
+          _ptr(q, "q", FP8, (rows, C)), _ptr(scale, "scale", torch.float32, ((C + 127) // 128, rows)))
+    return q
+
+
+def veda_quant_fp8_weight(w: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, stream=None) -> torch.Tensor:
+    """A weight [N, K] to e4m3 with a scale per 128 x 128 block, [ceil(N/128), ceil(K/128)]."""
+    if w.dim() != 2:
+        raise ValueError("w must be [N, K]")
+    N, K = w.shape
+    _call("veda_quant_fp8_weight", (w, q, scale), stream, N, K, _type(w, "w"), _ptr(w, "w"),
+          _ptr(q, "q", FP8, (N, K)), _ptr(scale, "scale", torch.float32, ((N + 127) // 128, (K + 127) // 128)))
+    return q
+
+
+def veda_gemm_fp8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor,
+                  bias: Optional[torch.Tensor], out: torch.Tensor, stream=None) -> torch.Tensor:
+    """out [M, N] = a [M, K] b [N, K]^T (+ bias) of e4m3 operands with a scale per row and 128 channels of a,
+    [ceil(K/128), M], and per 128 x 128 block of b, [ceil(N/128), ceil(K/128)]; out bf16 or fp32."""
+    ap, lda = _rows(a, "a")
+    bp, ldb = _rows(b, "b")
+    (M, K), N = a.shape, b.shape[0]
+    if a.dtype != FP8 or b.dtype != FP8:
+        raise ValueError(f"a and b must be {FP8} (got {a.dtype} and {b.dtype})")
+    if b.shape[1] != K:
+        raise ValueError(f"b must be [N, {K}] (got {tuple(b.shape)})")
+    op, ldo = _rows(out, "out", (M, N))
+    kb = (K + 127) // 128
+    _call("veda_gemm_fp8", (a, a_scale, b, b_scale, bias, out), stream, M, N, K, ap, lda,
+          _ptr(a_scale, "a_scale", torch.float32, (kb, M)), bp, ldb,
+          _ptr(b_scale, "b_scale", torch.float32, ((N + 127) // 128, kb)), _ptr(bias, "bias", torch.float32, (N,)),
+          _type(out, "out"), op, ldo)
+    return out
+
+
+def veda_rope_table(table: torch.Tensor, theta: float = 10000.0, start: float = 0.0, step: float = 1.0,
+                    stream=None) -> torch.Tensor:
+    """(cos, sin) of (start + step*i) * theta^(-2j/dim) into table [n, dim/2, 2] fp32 (angles in fp64)."""
+    if table.dim() != 3 or table.shape[2] != 2:
+        raise ValueError("table must be [n, dim/2, 2]")
+    _call("veda_rope_table", (table,), stream, table.shape[0], 2 * table.shape[1], theta, start, step,
+          _ptr(table, "table", torch.float32))
+    return table
+
+
+def make_rope(B: int, heads: int, d: int, grid: Sequence[int], tables: Sequence[Optional[torch.Tensor]],
+              pairing: str = "interleaved", norm: str = "row", eps: float = 1e-6) -> veda_rope:
+    """C struct of a rotary description; tables (time, height, width): fp32 [at least the grid's size, pairs, 2]
+    device tensors, or None for an axis without channels.  The tensors must outlive the struct's use."""
+    if norm not in _NORMS:
+        raise ValueError(f"norm must be one of {sorted(_NORMS)} (got {norm!r})")
+    if pairing not in _PAIRINGS:
+        raise ValueError(f"pairing must be one of {sorted(_PAIRINGS)} (got {pairing!r})")
+    if len(grid) != 3 or len(tables) != 3:
+        raise ValueError("grid and tables have three entries: time, height, width")
+    dims, ptrs = [], []
+    for t, n in zip(tables, grid):
+        if t is not None and (t.dim() != 3 or t.shape[2] != 2 or t.shape[0] < n):
+            raise ValueError(f"a table must be [at least {n}, pairs, 2] (got {tuple(t.shape)})")
+        dims.append(0 if t is None else 2 * t.shape[1])
+        ptrs.append(None if t is None or t.shape[1] == 0 else _ptr(t, "table", torch.float32))
+    return veda_rope(B, heads, d, veda_grid(*grid), *dims, *ptrs, _PAIRINGS[pairing], _NORMS[norm], eps)
+
+
+def _tokens(t: Optional[torch.Tensor], r: veda_rope, name: str, dtype: torch.dtype) -> Optional[veda_tokens]:
+    if t is None:
+        return None
+    n = r.grid.T * r.grid.H * r.grid.W
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if tuple(t.shape) != (r.B, n, r.heads, r.d) or t.stride(3) != 1 or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} [{r.B}, {n}, {r.heads}, {r.d}] with contiguous channels "
+                         f"(got {t.dtype} {tuple(t.shape)})")
+    return veda_tokens(t.data_ptr(), t.stride(0) if r.B > 1 else 0, t.stride(1) if n > 1 else 0,
+                       t.stride(2) if r.heads > 1 else 0)
+
+
+def _ref(s):
+    return None if s is None else ctypes.byref(s)
+
+
+def _norm_weight(w: Optional[torch.Tensor], r: veda_rope, name: str) -> Optional[int]:
+    if r.norm == 0 or w is None:
+        return None
+    return _ptr(w, name, torch.float32, (r.heads * r.d if r.norm == 1 else r.d,))
+
+
+def _first(*ts):
+    return next((t for t in ts if t is not None), None)
+
+
+def veda_qkv_norm_rope(r: veda_rope, q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Optional[torch.Tensor],
+                       wq: Optional[torch.Tensor], wk: Optional[torch.Tensor], q_out: Optional[torch.Tensor],
+                       k_out: Optional[torch.Tensor], v_out: Optional[torch.Tensor], stream=None) -> None:
+    """Norm of q and k, rotary positions, and token order [B, N, heads, d] (any strides) -> grid order bf16."""
+    some = _first(q, k, v)
+    if some is None:
+        raise ValueError("one of q, k and v is needed")
+    shape = (r.B, r.heads, r.grid.T * r.grid.H * r.grid.W, r.d)
+    tk = [_tokens(t, r, n, some.dtype) for t, n in ((q, "q"), (k, "k"), (v, "v"))]
+    _call("veda_qkv_norm_rope", (q, k, v, wq, wk, q_out, k_out, v_out), stream, ctypes.byref(r), _type(some, "q, k, v"),
+          _ref(tk[0]), _ref(tk[1]), _ref(tk[2]), _norm_weight(wq, r, "wq"), _norm_weight(wk, r, "wk"),
+          _ptr(q_out, "q_out", torch.bfloat16, shape), _ptr(k_out, "k_out", torch.bfloat16, shape),
+          _ptr(v_out, "v_out", torch.bfloat16, shape))
+
+
+def veda_qkv_norm_rope_backward_workspace(r: veda_rope, device=None) -> int:
+    n = _SZ()
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    _on_device(dev, lambda: _check(LIB.veda_qkv_norm_rope_backward_workspace(ctypes.byref(r), ctypes.byref(n)),
+                                   "veda_qkv_norm_rope_backward_workspace"))
+    return int(n.value)
+
+
+def veda_qkv_norm_rope_backward(r: veda_rope, q: Optional[torch.Tensor], k: Optional[torch.Tensor],
+                                wq: Optional[torch.Tensor], wk: Optional[torch.Tensor], d_q: Optional[torch.Tensor],
+                                d_k: Optional[torch.Tensor], d_v: Optional[torch.Tensor], dq: Optional[torch.Tensor],
+                                dk: Optional[torch.Tensor], dv: Optional[torch.Tensor], dwq: Optional[torch.Tensor],
+                                dwk: Optional[torch.Tensor], workspace: Optional[torch.Tensor], stream=None) -> None:
+    """Gradients of veda_qkv_norm_rope for grid-order upstream gradients d_q, d_k, d_v: token-order dq, dk, dv
+    (strides of their own) and dwq, dwk.  An operand whose upstream gradient is None is left out."""
+    some = _first(dq, dk, dv)
+    if some is None:
+        raise ValueError("one of dq, dk and dv is needed")
+    shape = (r.B, r.heads, r.grid.T * r.grid.H * r.grid.W, r.d)
+    tk = [_tokens(t, r, n, some.dtype) for t, n in ((q, "q"), (k, "k"), (dq, "dq"), (dk, "dk"), (dv, "dv"))]
+    _call("veda_qkv_norm_rope_backward", (q, k, wq, wk, d_q, d_k, d_v, dq, dk, dv, dwq, dwk, workspace), stream,
+          ctypes.byref(r), _type(some, "dq, dk, dv"), _ref(tk[0]), _ref(tk[1]), _norm_weight(wq, r, "wq"),
+          _norm_weight(wk, r, "wk"), _ptr(d_q, "d_q", torch.bfloat16, shape), _ptr(d_k, "d_k", torch.bfloat16, shape),
+          _ptr(d_v, "d_v", torch.bfloat16, shape), _ref(tk[2]), _ref(tk[3]), _ref(tk[4]),
+          _norm_weight(dwq, r, "dwq"), _norm_weight(dwk, r, "dwk"), _ptr(workspace, "workspace"),
+          0 if workspace is None else workspace.numel() * workspace.element_size())
 
 
 def veda_sync_status(stream=None) -> None:

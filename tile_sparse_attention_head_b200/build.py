@@ -19,7 +19,8 @@ LIB = os.path.join(HERE, "libveda.so")
 # binding loads it instead of LIB when VEDA_DEBUG_BOUNDS=1 is set.
 DEBUG_LIB = os.path.join(HERE, "libveda_debug.so")
 SOURCES = ["veda_api.cu", "veda_common.cuh", "kernels.h", "permute_tripool.cu", "score_topk.cu",
-           "sparse_attn.cu", "tile_map.cu", "estimator.cu", "distill.cu", "attn_bwd.cu"]
+           "sparse_attn.cu", "tile_map.cu", "estimator.cu", "distill.cu", "attn_bwd.cu", "layer_common.cuh",
+           "rms_norm.cu", "qkv_rope.cu", "quant_fp8.cu", "gemm_fp8.cu", "layer_api.cu"]
 
 
 def nvcc_path() -> str:

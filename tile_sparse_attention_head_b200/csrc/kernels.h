@@ -143,6 +143,86 @@ cudaError_t launch_attn_bwd_dq(const Geometry& G, const BwdMaps<kMaxGridMaps>& m
 cudaError_t launch_attn_bwd_dkdv(const Geometry& G, const BwdMaps<kMaxGridMaps>& m, const BwdArgs& a,
                                  cudaStream_t s);
 
+// ---- operators around the attention ----
+
+struct NormArgs {
+  long long rows;
+  int C;
+  const void* x;       // [rows, C], row stride ldx elements
+  long long ldx;
+  const void* delta;   // [rows, C], row stride ldd; or null (h = x)
+  long long ldd;
+  const float* w;
+  float eps;
+  void* h;             // [rows, C] or null
+  void* y;             // [rows, C] in delta's type, or e4m3
+  float* scale;        // e4m3 only: [ceil(C/128), rows]
+  float* rstd;         // [rows] or null
+  int warps;           // per row
+};
+
+struct NormBwdArgs {
+  long long rows;
+  int C;
+  const void *h, *dy, *dh;
+  const float *w, *rstd;
+  void *dx, *ddelta;   // either may be null
+  float* part;         // [parts, C] or null
+  int parts, warps;
+};
+
+struct RopeArgs {
+  int heads, d, H, W, N;
+  long long tokens;             // B * N
+  int norm, halves;
+  float eps;
+  int dim[3];
+  const float2* tab[3];
+  const float* w[3];
+  const void* in[3];
+  void* out[3];                 // grid order: written forward, read backward
+  void* dx[3];                  // backward
+  long long sb[3], sn[3], sh[3], dsb[3], dsn[3], dsh[3];   // element strides of in and dx
+  float* part[3];
+  int parts, warps;
+  int order[3];                 // the operands of this launch: 0 Q, 1 K, 2 V
+};
+
+struct QuantArgs {
+  const void* x;
+  long long rows, N;            // rows = batches * N
+  int C, d;
+  long long sb, sn, sh;
+  uint8_t* q;
+  float* scale;
+};
+
+struct GemmArgs {
+  int M, N, K, kblocks, nblocks;
+  const float *sa, *sb, *bias;
+  void* out;
+  long long ldo;
+  uint64_t timeout_ns;
+  int tiles_m, tiles_n, tiles;
+};
+
+cudaError_t launch_add_rms_norm(NormArgs a, int tx, int td, bool fp8, int sms, cudaStream_t s);
+int add_rms_norm_bwd_parts(long long rows, int C, int sms);
+cudaError_t launch_add_rms_norm_bwd(NormBwdArgs a, int tx, int td, float* dw, int sms, cudaStream_t s);
+cudaError_t launch_sum_partials(const float* part, int parts, int C, float* out, cudaStream_t s);
+
+cudaError_t launch_qkv_rope(RopeArgs a, int type, int n_which, int sms, cudaStream_t s);
+int qkv_rope_bwd_parts(long long tokens, int heads, int d, bool row, int sms);
+cudaError_t launch_qkv_rope_bwd(RopeArgs a, int type, int n_which, float* const* dw, int sms, cudaStream_t s);
+cudaError_t launch_rope_table(int n, int dim, double theta, double start, double step, float* out, cudaStream_t s);
+
+cudaError_t launch_quant_rows(const QuantArgs& a, int type, cudaStream_t s);
+cudaError_t launch_quant_weight(const void* w, int type, int N, int K, uint8_t* q, float* scale, cudaStream_t s);
+
+void gemm_fp8_boxes(const GemmArgs& a, int* rows_a, int* rows_b);
+cudaError_t launch_gemm_fp8(const CUtensorMap& ta, const CUtensorMap& tb, const GemmArgs& a, int out_type, int sms,
+                            cudaStream_t s);
+
 cudaError_t launch_timeout_selftest(uint64_t timeout_ns, cudaStream_t s);
 cudaError_t launch_bounds_selftest(cudaStream_t s);
 

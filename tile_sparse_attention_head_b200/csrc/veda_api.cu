@@ -21,6 +21,10 @@
 #include "tile_map.cu"
 #include "distill.cu"
 #include "attn_bwd.cu"
+#include "rms_norm.cu"
+#include "qkv_rope.cu"
+#include "quant_fp8.cu"
+#include "gemm_fp8.cu"
 
 namespace veda {
 namespace {
@@ -848,10 +852,11 @@ veda_status veda_sync_status(void* stream) {
       return fail(VEDA_ERR_CUDA, "a kernel found its dynamic shared memory base not 1024-byte aligned");
     if (word == kErrBounds) {
       static const char* const files[] = {"?", "permute_tripool.cu", "score_topk.cu", "estimator.cu",
-                                          "sparse_attn.cu", "tile_map.cu", "attn_bwd.cu", "distill.cu"};
+                                          "sparse_attn.cu", "tile_map.cu", "attn_bwd.cu", "distill.cu",
+                                          "rms_norm.cu", "qkv_rope.cu", "quant_fp8.cu", "gemm_fp8.cu"};
       const int f = site / 10000;
       return fail(VEDA_ERR_BOUNDS, "debug bounds check failed at %s:%d; the access was skipped",
-                  files[(f >= 0 && f < 8) ? f : 0], site % 10000);
+                  files[(f >= 0 && f < (int)(sizeof(files) / sizeof(files[0]))) ? f : 0], site % 10000);
     }
     return fail(VEDA_ERR_TIMEOUT, "a kernel gave up on a bounded wait (device error word %d)", word);
   }
@@ -892,3 +897,5 @@ veda_status veda_selftest_bounds(void* stream) {
 }
 
 }  // extern "C"
+
+#include "layer_api.cu"

@@ -1,0 +1,334 @@
+"""The operators on both sides of the tile-sparse attention in a transformer
+layer, as torch functions over the C ABI, and the attention block they form.
+
+    h, y8 = add_rms_norm_fp8(x, delta)      residual + RMS norm, e4m3 with a scale per 128 channels
+    qkv   = gemm_fp8(y8, Wqkv)              8-bit product, a scale per block of 128
+    q, k, v = qkv_norm_rope(qkv)            Q/K norm, three-axis rotary positions, grid order
+    o     = VedaAttention(q, k, v)
+    delta = gemm_fp8(quant_fp8_heads(o), Wo)
+
+``add_rms_norm`` and ``qkv_norm_rope`` are differentiable torch ops (their
+backward runs in the library); the 8-bit forms are for inference and refuse
+inputs that ask for a gradient.  ``VedaSelfAttention`` chains the calls.
+Everything runs on the current stream of the tensors' device.
+"""
+from __future__ import annotations
+
+from typing import Optional, Sequence, Tuple
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import binding as B
+
+
+def _no_grad_inputs(func: str, *tensors) -> None:
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise ValueError(f"{func} is an inference operator: it has no gradient (call it under torch.no_grad())")
+
+
+def _wants_grad(*tensors) -> bool:
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+def _flat(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    """[..., C] as rows [R, C] with contiguous channels (a copy only if the strides need one)."""
+    if t is None:
+        return None
+    if t.dim() != 2:
+        t = t.reshape(t.numel() // t.shape[-1] if t.shape[-1] else 0, t.shape[-1])
+    return t if t.shape[1] <= 1 or t.stride(1) == 1 else t.contiguous()
+
+
+def _dense(t: Optional[torch.Tensor], shape, dtype: Optional[torch.dtype] = None) -> Optional[torch.Tensor]:
+    """An upstream gradient as the library reads it: dense, 16-byte aligned, of `shape`."""
+    if t is None:
+        return None
+    t = t.to(dtype or t.dtype).reshape(shape).contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+def _check_stream_and_delta(x: torch.Tensor, delta: Optional[torch.Tensor]) -> None:
+    if delta is not None and delta.shape != x.shape:
+        raise ValueError(f"delta must have x's shape {tuple(x.shape)} (got {tuple(delta.shape)})")
+
+
+# ---------------------------------------------------------------- residual and norm
+
+def _norm_forward(x, delta, weight, eps, want_rstd):
+    h = torch.empty(x.shape, dtype=x.dtype, device=x.device) if delta is not None else None
+    y = torch.empty(x.shape, dtype=x.dtype if delta is None else delta.dtype, device=x.device)
+    rstd = torch.empty(x.shape[0], dtype=torch.float32, device=x.device) if want_rstd else None
+    B.veda_add_rms_norm(x, delta, weight, eps, h, y, rstd)
+    return h, y, rstd
+
+
+class _AddRmsNorm(torch.autograd.Function):
+    """(h, y) of residual addition and RMS norm; without a delta, y alone."""
+
+    @staticmethod
+    def forward(ctx, x, delta, weight, eps):
+        x2, d2 = _flat(x), _flat(delta)
+        h, y, rstd = _norm_forward(x2, d2, weight, eps, True)
+        if delta is None:
+            h = x2 if x2.is_contiguous() else x2.contiguous()
+        ctx.has_delta = delta is not None
+        ctx.delta_type = y.dtype
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(h, weight, rstd)
+        y = y.view(x.shape)
+        return (h.view(x.shape), y) if ctx.has_delta else y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, *grads):
+        h, weight, rstd = ctx.saved_tensors
+        dh, dy = grads if ctx.has_delta else (None, grads[0])
+        want_x, want_d, want_w, _ = ctx.needs_input_grad
+        shape = h.shape if dy is None and dh is None else (dh if dy is None else dy).shape
+        if dy is None:   # only the sum itself was used: its gradient goes to both addends
+            return dh if want_x else None, None if dh is None or not want_d else dh.to(ctx.delta_type), None, None
+        dy, dh = _dense(dy, h.shape), _dense(dh, h.shape)
+        same = dy.dtype == h.dtype
+        dx = torch.empty_like(h) if want_x or (want_d and same) else None
+        dd = torch.empty_like(dy) if want_d and not same else None
+        dw = ws = None
+        if want_w:
+            dw = torch.empty_like(weight)
+            ws = torch.empty(B.veda_add_rms_norm_backward_workspace(*h.shape, h.device), dtype=torch.uint8,
+                             device=h.device)
+        B.veda_add_rms_norm_backward(h, dy, dh, weight, rstd, dx, dd, dw, ws)
+        gx = None if dx is None else dx.view(shape)
+        gd = gx if same else None if dd is None else dd.view(shape)
+        return gx if want_x else None, gd if want_d else None, dw, None
+
+
+def add_rms_norm(x: torch.Tensor, delta: Optional[torch.Tensor], weight: torch.Tensor,
+                 eps: float = 1e-6) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(h, y): h = x + delta in x's type and y = h * (mean_c h^2 + eps)^(-1/2) * weight in delta's type.
+
+    x and delta [..., C] of one type (bf16, fp16, fp32), or an fp32 residual
+    stream x with a bf16 delta; weight [C] fp32.  delta None: h is x.  The norm
+    is taken of the rounded h.  Differentiable in x, delta and weight."""
+    _check_stream_and_delta(x, delta)
+    if not _wants_grad(x, delta, weight):
+        h, y, _ = _norm_forward(_flat(x), _flat(delta), weight, eps, False)
+        return (x if h is None else h.view(x.shape)), y.view(x.shape)
+    if delta is None:
+        return x, _AddRmsNorm.apply(x, None, weight, eps)
+    return _AddRmsNorm.apply(x, delta, weight, eps)
+
+
+def add_rms_norm_fp8(x: torch.Tensor, delta: Optional[torch.Tensor], weight: torch.Tensor,
+                     eps: float = 1e-6) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(h, y8, y_scale): add_rms_norm with y as e4m3 rows [R, C] and scales [ceil(C/128), R] for gemm_fp8."""
+    _no_grad_inputs("add_rms_norm_fp8", x, delta, weight)
+    _check_stream_and_delta(x, delta)
+    x2, d2 = _flat(x), _flat(delta)
+    rows, C = x2.shape
+    h = torch.empty((rows, C), dtype=x.dtype, device=x.device) if delta is not None else None
+    y8 = torch.empty((rows, C), dtype=B.FP8, device=x.device)
+    scale = torch.empty(((C + 127) // 128, rows), dtype=torch.float32, device=x.device)
+    B.veda_add_rms_norm_fp8(x2, d2, weight, eps, h, y8, scale)
+    return (x if h is None else h.view(x.shape)), y8, scale
+
+
+# ---------------------------------------------------------------- 8-bit product
+
+def quant_fp8(x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
+    """[..., C] -> e4m3 rows [R, C] and a scale per row and 128 channels, [ceil(C/128), R]."""
+    _no_grad_inputs("quant_fp8", x)
+    return _quant(_flat(x))
+
+
+def quant_fp8_heads(o: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The attention's grid-order output [B, heads, N, d] -> e4m3 rows [B*N, heads*d] and their scales."""
+    _no_grad_inputs("quant_fp8_heads", o)
+    if o.dim() != 4:
+        raise ValueError("o must be [B, heads, N, d]")
+    return _quant(o)
+
+
+def _quant(x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
+    rows, C = x.shape if x.dim() == 2 else (x.shape[0] * x.shape[2], x.shape[1] * x.shape[3])
+    q = torch.empty((rows, C), dtype=B.FP8, device=x.device)
+    scale = torch.empty(((C + 127) // 128, rows), dtype=torch.float32, device=x.device)
+    B.veda_quant_fp8(x, q, scale)
+    return q, scale
+
+
+def quant_fp8_weight(w: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
+    """A linear layer's weight [N, K] -> e4m3 and a scale per 128 x 128 block, [ceil(N/128), ceil(K/128)]."""
+    w = w.detach().contiguous()
+    q = torch.empty(w.shape, dtype=B.FP8, device=w.device)
+    scale = torch.empty(((w.shape[0] + 127) // 128, (w.shape[1] + 127) // 128), dtype=torch.float32, device=w.device)
+    B.veda_quant_fp8_weight(w, q, scale)
+    return q, scale
+
+
+def gemm_fp8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor,
+             bias: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+             out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """[M, N] = a [M, K] @ b [N, K]^T (+ bias fp32 [N]) of e4m3 operands with a scale for each block of 128."""
+    _no_grad_inputs("gemm_fp8", a_scale, b_scale, bias)
+    if out is None:
+        out = torch.empty((a.shape[0], b.shape[0]), dtype=out_dtype, device=a.device)
+    return B.veda_gemm_fp8(a, a_scale, b, b_scale, bias, out)
+
+
+# ---------------------------------------------------------------- rotary positions
+
+def rope_table(n: int, dim: int, theta: float = 10000.0, start: float = 0.0, step: float = 1.0,
+               device="cuda") -> torch.Tensor:
+    """(cos, sin) of n positions start + step*i for one axis of `dim` channels: fp32 [n, dim/2, 2], angles in fp64."""
+    return B.veda_rope_table(torch.empty((n, dim // 2, 2), dtype=torch.float32, device=device), theta, start, step)
+
+
+def rope_tables(grid: Sequence[int], dims: Sequence[int], theta: float = 10000.0,
+                start: Sequence[float] = (0.0, 0.0, 0.0), step: Sequence[float] = (1.0, 1.0, 1.0),
+                device="cuda") -> Tuple[Optional[torch.Tensor], ...]:
+    """The (time, height, width) tables of a grid; dims: channels of each axis (None for an axis with none)."""
+    return tuple(rope_table(n, dim, theta, a, b, device) if dim else None
+                 for n, dim, a, b in zip(grid, dims, start, step))
+
+
+class _QkvNormRope(torch.autograd.Function):
+    """q, k, v in grid order from one packed tensor or from three."""
+
+    @staticmethod
+    def forward(ctx, rope, tables, wq, wk, *xs):
+        q, k, v = xs[0].unbind(2) if len(xs) == 1 else xs
+        shape = (rope.B, rope.heads, q.shape[1], rope.d)
+        outs = tuple(torch.empty(shape, dtype=torch.bfloat16, device=q.device) for _ in range(3))
+        B.veda_qkv_norm_rope(rope, q, k, v, wq, wk, *outs)
+        ctx.rope, ctx.tables, ctx.packed = rope, tables, len(xs) == 1     # tables: kept alive for backward
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(wq, wk, *xs)
+        return outs
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, *douts):
+        rope = ctx.rope
+        wq, wk, *xs = ctx.saved_tensors
+        want_wq, want_wk, *want_x = ctx.needs_input_grad[2:]
+        if ctx.packed:
+            x = xs[0]
+            packed = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            for i, g in enumerate(douts):
+                if g is None:
+                    packed[:, :, i].zero_()
+            q, k, v = x.unbind(2)
+            dxs = list(packed.unbind(2))
+        else:
+            q, k, v = xs
+            dxs = [None if g is None else torch.empty(q.shape, dtype=q.dtype, device=q.device) for g in douts]
+        need = [g is not None for g in douts]
+        if any(need):
+            d = [_dense(g, (rope.B, rope.heads, q.shape[1], rope.d), torch.bfloat16) for g in douts]
+            dwq = torch.empty_like(wq) if want_wq and need[0] else None
+            dwk = torch.empty_like(wk) if want_wk and need[1] else None
+            ws = None
+            if dwq is not None or dwk is not None:
+                ws = torch.empty(B.veda_qkv_norm_rope_backward_workspace(rope, q.device), dtype=torch.uint8,
+                                 device=q.device)
+            B.veda_qkv_norm_rope_backward(rope, q, k, wq, wk, *d, *(x if n else None for x, n in zip(dxs, need)),
+                                          dwq, dwk, ws)
+        else:
+            dwq = dwk = None
+        dx = (packed if want_x[0] else None,) if ctx.packed else tuple(x if w else None for x, w in zip(dxs, want_x))
+        return (None, None, dwq, dwk) + dx
+
+
+def qkv_norm_rope(qkv, grid: Sequence[int], tables: Sequence[Optional[torch.Tensor]],
+                  wq: Optional[torch.Tensor] = None, wk: Optional[torch.Tensor] = None, norm: str = "row",
+                  eps: float = 1e-6,
+                  pairing: str = "interleaved") -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """q, k, v [B, heads, N, d] bf16 for the attention from the QKV product.
+
+    qkv: one packed tensor [B, N, 3, heads, d], or (q, k, v), each [B, N, heads,
+    d]; bf16, fp16 or fp32, channels contiguous, other strides free multiples of
+    8.  grid: (T, H, W) with N = T*H*W.  tables: (cos, sin) per axis (rope_tables);
+    a table from a later row on moves the grid along that axis.  norm: RMS norm
+    of q and k over all channels of a token ("row", weights [heads*d] fp32), over
+    each head ("head", weights [d]) or "none".  pairing: "interleaved" or
+    "halves" of each axis's channels.  Differentiable in qkv, wq and wk."""
+    if isinstance(qkv, torch.Tensor):
+        if qkv.dim() != 5 or qkv.shape[2] != 3:
+            raise ValueError(f"qkv must be [B, N, 3, heads, d] (got {tuple(qkv.shape)})")
+        xs = (qkv,)
+        b, n, _, heads, d = qkv.shape
+    else:
+        xs = tuple(qkv)
+        if len(xs) != 3 or any(t.dim() != 4 for t in xs):
+            raise ValueError("qkv must be a packed tensor or (q, k, v), each [B, N, heads, d]")
+        b, n, heads, d = xs[0].shape
+    grid = tuple(int(g) for g in grid)
+    if len(grid) != 3 or n != grid[0] * grid[1] * grid[2]:
+        raise ValueError(f"N = {n} tokens do not fill the grid {grid}")
+    if norm != "none" and (wq is None or wk is None):
+        raise ValueError(f"norm {norm!r} needs wq and wk")
+    if norm == "none" and (wq is not None or wk is not None):
+        raise ValueError("norm 'none' takes no weights")
+    for t in tables:
+        if t is not None and t.device != xs[0].device:
+            raise ValueError(f"a table is on {t.device}, qkv on {xs[0].device}")
+    rope = B.make_rope(b, heads, d, grid, tables, pairing, norm, eps)
+    if _wants_grad(wq, wk, *xs):
+        return _QkvNormRope.apply(rope, tuple(tables), wq, wk, *xs)
+    q, k, v = xs[0].unbind(2) if len(xs) == 1 else xs
+    outs = tuple(torch.empty((b, heads, n, d), dtype=torch.bfloat16, device=q.device) for _ in range(3))
+    B.veda_qkv_norm_rope(rope, q, k, v, wq, wk, *outs)
+    return outs
+
+
+# ---------------------------------------------------------------- the attention block
+
+class VedaSelfAttention:
+    """The attention block of a video transformer layer for inference, in 8-bit products:
+
+        (x, delta) -> h = x + delta;  out = Wo attention(norm(h) Wqkv^T)
+
+    ``attention`` is a VedaAttention; weights are given in bf16, fp16 or fp32
+    and laid out in e4m3 once: w_qkv [3*heads*d, C], w_o [C, heads*d], biases fp32
+    or None, norm_weight [C], wq and wk the Q/K norm's weights (see qkv_norm_rope).
+    The residual stream goes through unchanged in type; ``out`` (bf16) is the
+    delta of the next block."""
+
+    def __init__(self, attention, w_qkv: torch.Tensor, w_o: torch.Tensor, norm_weight: torch.Tensor,
+                 tables: Sequence[Optional[torch.Tensor]], wq: Optional[torch.Tensor] = None,
+                 wk: Optional[torch.Tensor] = None, b_qkv: Optional[torch.Tensor] = None,
+                 b_o: Optional[torch.Tensor] = None, norm: str = "row", eps: float = 1e-6,
+                 pairing: str = "interleaved"):
+        p = attention.p
+        inner, C = p.heads * p.d, norm_weight.shape[0]
+        if tuple(w_qkv.shape) != (3 * inner, C) or tuple(w_o.shape) != (C, inner):
+            raise ValueError(f"w_qkv must be [{3 * inner}, {C}] and w_o [{C}, {inner}] "
+                             f"(got {tuple(w_qkv.shape)} and {tuple(w_o.shape)})")
+        self.att, self.p, self.C = attention, p, C
+        self.w_qkv, self.s_qkv = quant_fp8_weight(w_qkv)
+        self.w_o, self.s_o = quant_fp8_weight(w_o)
+        self.b_qkv, self.b_o = b_qkv, b_o
+        self.norm_weight, self.wq, self.wk = norm_weight, wq, wk
+        self.tables, self.norm, self.eps, self.pairing = tuple(tables), norm, eps, pairing
+
+    @torch.no_grad()
+    def __call__(self, x: torch.Tensor, delta: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+        """x, delta [B, N, C] -> (h [B, N, C] in x's type, out [B, N, C] bf16).
+
+        One call at a time per object: the attention's selection and workspace are its own."""
+        p = self.p
+        if tuple(x.shape) != (p.B, p.N, self.C):
+            raise ValueError(f"x must be [{p.B}, {p.N}, {self.C}] (got {tuple(x.shape)})")
+        if x.device != self.w_qkv.device:
+            raise ValueError(f"x is on {x.device}, the weights on {self.w_qkv.device}")
+        return B._on_device(x.device, lambda: self._run(x, delta))
+
+    def _run(self, x, delta):
+        p = self.p
+        h, y, ys = add_rms_norm_fp8(x, delta, self.norm_weight, self.eps)
+        qkv = gemm_fp8(y, ys, self.w_qkv, self.s_qkv, self.b_qkv)
+        q, k, v = qkv_norm_rope(qkv.view(p.B, p.N, 3, p.heads, p.d), p.grid, self.tables, self.wq, self.wk, self.norm,
+                                self.eps, self.pairing)
+        o, os = quant_fp8_heads(self.att(q, k, v))
+        return h, gemm_fp8(o, os, self.w_o, self.s_o, self.b_o).view(p.B, p.N, self.C)
