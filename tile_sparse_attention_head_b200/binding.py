@@ -424,12 +424,16 @@ def veda_head_error(p: Problem, o: torch.Tensor, o_ref: torch.Tensor, err: torch
 # ---------------------------------------------------------------- around the attention
 #
 # These take tensors of any device: the call runs on its tensors' device (all on
-# one) and, without a `stream`, on that device's current stream.
+# one) and, without a `stream`, on that device's current stream.  A call on one
+# token takes a few microseconds on the GPU, so what runs on the host around it
+# is kept short: device, stream and shape are compared as plain integers and
+# tuples, and messages are put together only when something is refused.
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _NORMS = {"none": 0, "row": 1, "head": 2}
 _PAIRINGS = {"interleaved": 0, "halves": 1}
 FP8 = torch.float8_e4m3fn
+_F32 = torch.float32
 
 
 def _type(t: torch.Tensor, name: str) -> int:
@@ -439,41 +443,55 @@ def _type(t: torch.Tensor, name: str) -> int:
     return code
 
 
-def _rows(t: Optional[torch.Tensor], name: str, shape=None) -> Tuple[Optional[int], int]:
+def _device(t: torch.Tensor, name: str) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev
+
+
+def _at(t: Optional[torch.Tensor], name: str, dev: int, dtype: torch.dtype, shape: Tuple[int, ...]) -> Optional[int]:
+    """Pointer of a dense tensor of this device, type and shape."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the first operand on cuda:{dev}" if t.is_cuda
+                         else f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _ptr(t, name, dtype, shape)      # says what is wrong
+    return t.data_ptr()
+
+
+def _rows(t: Optional[torch.Tensor], name: str, dev: int, shape=None) -> Tuple[Optional[int], int]:
     """Pointer and row stride of a [rows, C] tensor whose channels are contiguous."""
     if t is None:
         return None, 0
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the first operand on cuda:{dev}" if t.is_cuda
+                         else f"{name} must be a CUDA tensor")
+    size = t.shape
+    if len(size) != 2 or (size[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{name} must be [rows, C] with contiguous channels")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if shape is not None and size != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(size)})")
+    return t.data_ptr(), t.stride(0) if size[0] > 1 else size[1]
 
 
-def _call(func: str, tensors, stream, *args) -> None:
-    """Runs the library function on the device of `tensors` (None entries are skipped)."""
-    dev = None
-    for t in tensors:
-        if t is not None:
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise ValueError(f"{func}: tensors are on {dev} and {t.device}")
-    fn = getattr(LIB, func)
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)), func)
-    else:
+def _call(func: str, dev: int, stream, *args) -> None:
+    """Runs the library function with `dev` current, on `stream` or that device's current stream."""
+    if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
-            _check(fn(*args, _stream(stream)), func)
+            return _call(func, dev, stream, *args)
+    status = getattr(LIB, func)(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    if status != VEDA_OK:
+        _check(status, func)
 
 
-def _on_device(dev: torch.device, fn):
-    """fn() with `dev` current (the workspace sizes depend on the device)."""
-    if dev.index == torch.cuda.current_device():
+def _on_device(device, fn):
+    """fn() with `device` (None: the current one) current: the workspace sizes depend on it."""
+    if device is None or device == torch._C._cuda_getDevice():
         return fn()
-    with torch.cuda.device(dev):
+    with torch.cuda.device(device):
         return fn()
 
 
@@ -481,13 +499,13 @@ def veda_add_rms_norm(x: torch.Tensor, delta: Optional[torch.Tensor], weight: to
                       h: Optional[torch.Tensor], y: torch.Tensor, rstd: Optional[torch.Tensor] = None,
                       stream=None) -> torch.Tensor:
     """h = x + delta and its RMS norm y, [rows, C]; y is of delta's type (x's without a delta)."""
-    xp, ldx = _rows(x, "x")
-    dp, ldd = _rows(delta, "delta", x.shape)
-    rows, C = x.shape
-    td = _type(y if delta is None else delta, "y" if delta is None else "delta")
-    _call("veda_add_rms_norm", (x, delta, weight, h, y, rstd), stream, rows, C, _type(x, "x"), xp, ldx, td, dp, ldd,
-          _ptr(weight, "weight", torch.float32, (C,)), eps, _ptr(h, "h", x.dtype, x.shape),
-          _ptr(y, "y", y.dtype if delta is None else delta.dtype, x.shape), _ptr(rstd, "rstd", torch.float32, (rows,)))
+    dev, shape = _device(x, "x"), x.shape
+    xp, ldx = _rows(x, "x", dev)
+    dp, ldd = _rows(delta, "delta", dev, shape)
+    td = y.dtype if delta is None else delta.dtype
+    _call("veda_add_rms_norm", dev, stream, shape[0], shape[1], _type(x, "x"), xp, ldx,
+          _type(y, "y") if delta is None else _type(delta, "delta"), dp, ldd, _at(weight, "weight", dev, _F32, shape[1:]),
+          eps, _at(h, "h", dev, x.dtype, shape), _at(y, "y", dev, td, shape), _at(rstd, "rstd", dev, _F32, shape[:1]))
     return y
 
 
@@ -495,23 +513,23 @@ def veda_add_rms_norm_fp8(x: torch.Tensor, delta: Optional[torch.Tensor], weight
                           h: Optional[torch.Tensor], y8: torch.Tensor, y_scale: torch.Tensor,
                           stream=None) -> torch.Tensor:
     """veda_add_rms_norm with y in e4m3 and a scale per row and 128 channels, [ceil(C/128), rows]."""
-    xp, ldx = _rows(x, "x")
-    dp, ldd = _rows(delta, "delta", x.shape)
-    rows, C = x.shape
+    dev, shape = _device(x, "x"), x.shape
+    xp, ldx = _rows(x, "x", dev)
+    dp, ldd = _rows(delta, "delta", dev, shape)
+    rows, C = shape
     tx = _type(x, "x")
-    _call("veda_add_rms_norm_fp8", (x, delta, weight, h, y8, y_scale), stream, rows, C, tx, xp, ldx,
-          tx if delta is None else _type(delta, "delta"), dp, ldd, _ptr(weight, "weight", torch.float32, (C,)), eps,
-          _ptr(h, "h", x.dtype, x.shape), _ptr(y8, "y8", FP8, x.shape),
-          _ptr(y_scale, "y_scale", torch.float32, ((C + 127) // 128, rows)))
+    _call("veda_add_rms_norm_fp8", dev, stream, rows, C, tx, xp, ldx,
+          tx if delta is None else _type(delta, "delta"), dp, ldd, _at(weight, "weight", dev, _F32, (C,)), eps,
+          _at(h, "h", dev, x.dtype, shape), _at(y8, "y8", dev, FP8, shape),
+          _at(y_scale, "y_scale", dev, _F32, ((C + 127) // 128, rows)))
     return y8
 
 
 def veda_add_rms_norm_backward_workspace(rows: int, C: int, device=None) -> int:
     n = _SZ()
-    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    _on_device(dev, lambda: _check(LIB.veda_add_rms_norm_backward_workspace(rows, C, ctypes.byref(n)),
-                                   "veda_add_rms_norm_backward_workspace"))
-    return int(n.value)
+    _on_device(device, lambda: _check(LIB.veda_add_rms_norm_backward_workspace(rows, C, ctypes.byref(n)),
+                                      "veda_add_rms_norm_backward_workspace"))
+    return n.value
 
 
 def veda_add_rms_norm_backward(h: torch.Tensor, dy: torch.Tensor, dh: Optional[torch.Tensor], weight: torch.Tensor,
@@ -519,23 +537,27 @@ def veda_add_rms_norm_backward(h: torch.Tensor, dy: torch.Tensor, dh: Optional[t
                                dweight: Optional[torch.Tensor], workspace: Optional[torch.Tensor],
                                stream=None) -> None:
     """Gradients of veda_add_rms_norm: dx in h's type, ddelta in dy's type, dweight fp32; None leaves one out."""
-    shape = h.shape
-    if h.dim() != 2:
+    dev, shape = _device(h, "h"), h.shape
+    if len(shape) != 2:
         raise ValueError("h must be [rows, C]")
-    rows, C = shape
-    _call("veda_add_rms_norm_backward", (h, dy, dh, weight, rstd, dx, ddelta, dweight, workspace), stream, rows, C,
-          _type(h, "h"), _ptr(h, "h"), _type(dy, "dy"), _ptr(dy, "dy", None, shape), _ptr(dh, "dh", h.dtype, shape),
-          _ptr(weight, "weight", torch.float32, (C,)), _ptr(rstd, "rstd", torch.float32, (rows,)),
-          _ptr(dx, "dx", h.dtype, shape), _ptr(ddelta, "ddelta", dy.dtype, shape),
-          _ptr(dweight, "dweight", torch.float32, (C,)), _ptr(workspace, "workspace"),
-          0 if workspace is None else workspace.numel() * workspace.element_size())
+    th, td = h.dtype, dy.dtype
+    _call("veda_add_rms_norm_backward", dev, stream, shape[0], shape[1], _type(h, "h"), _at(h, "h", dev, th, shape),
+          _type(dy, "dy"), _at(dy, "dy", dev, td, shape), _at(dh, "dh", dev, th, shape),
+          _at(weight, "weight", dev, _F32, shape[1:]), _at(rstd, "rstd", dev, _F32, shape[:1]),
+          _at(dx, "dx", dev, th, shape), _at(ddelta, "ddelta", dev, td, shape),
+          _at(dweight, "dweight", dev, _F32, shape[1:]), *_scratch(workspace, dev))
+
+
+def _scratch(workspace: Optional[torch.Tensor], dev: int) -> Tuple[Optional[int], int]:
+    if workspace is None:
+        return None, 0
+    return _at(workspace, "workspace", dev, workspace.dtype, workspace.shape), workspace.numel() * workspace.element_size()
 
 
 def veda_quant_fp8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, stream=None) -> torch.Tensor:
     """[rows, C], or the attention's grid-order [B, heads, N, d], to e4m3 rows [rows, C] (B*N rows of heads*d
     channels) and scales [ceil(C/128), rows].  Channels contiguous, other strides free multiples of 8."""
-    if not x.is_cuda:
-        raise ValueError("x must be a CUDA tensor")
+    dev = _device(x, "x")
     if x.dim() == 2:
         (N, d), (sn, sd) = x.shape, x.stride()
         B, heads, sb, sh = 1, 1, 0, 0
@@ -546,19 +568,20 @@ def veda_quant_fp8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, stream
     if d > 1 and sd != 1:
         raise ValueError("the channels of x must be contiguous")
     rows, C = B * N, heads * d
-    _call("veda_quant_fp8", (x, q, scale), stream, B, N, heads, d, _type(x, "x"), x.data_ptr(),
+    _call("veda_quant_fp8", dev, stream, B, N, heads, d, _type(x, "x"), x.data_ptr(),
           sb if B > 1 else 0, sn if N > 1 else 0, sh if heads > 1 else 0,
-          _ptr(q, "q", FP8, (rows, C)), _ptr(scale, "scale", torch.float32, ((C + 127) // 128, rows)))
+          _at(q, "q", dev, FP8, (rows, C)), _at(scale, "scale", dev, _F32, ((C + 127) // 128, rows)))
     return q
 
 
 def veda_quant_fp8_weight(w: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, stream=None) -> torch.Tensor:
     """A weight [N, K] to e4m3 with a scale per 128 x 128 block, [ceil(N/128), ceil(K/128)]."""
+    dev = _device(w, "w")
     if w.dim() != 2:
         raise ValueError("w must be [N, K]")
     N, K = w.shape
-    _call("veda_quant_fp8_weight", (w, q, scale), stream, N, K, _type(w, "w"), _ptr(w, "w"),
-          _ptr(q, "q", FP8, (N, K)), _ptr(scale, "scale", torch.float32, ((N + 127) // 128, (K + 127) // 128)))
+    _call("veda_quant_fp8_weight", dev, stream, N, K, _type(w, "w"), _at(w, "w", dev, w.dtype, (N, K)),
+          _at(q, "q", dev, FP8, (N, K)), _at(scale, "scale", dev, _F32, ((N + 127) // 128, (K + 127) // 128)))
     return q
 
 
@@ -566,18 +589,18 @@ def veda_gemm_fp8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_sca
                   bias: Optional[torch.Tensor], out: torch.Tensor, stream=None) -> torch.Tensor:
     """out [M, N] = a [M, K] b [N, K]^T (+ bias) of e4m3 operands with a scale per row and 128 channels of a,
     [ceil(K/128), M], and per 128 x 128 block of b, [ceil(N/128), ceil(K/128)]; out bf16 or fp32."""
-    ap, lda = _rows(a, "a")
-    bp, ldb = _rows(b, "b")
+    dev = _device(a, "a")
+    ap, lda = _rows(a, "a", dev)
+    bp, ldb = _rows(b, "b", dev)
     (M, K), N = a.shape, b.shape[0]
-    if a.dtype != FP8 or b.dtype != FP8:
+    if a.dtype is not FP8 or b.dtype is not FP8:
         raise ValueError(f"a and b must be {FP8} (got {a.dtype} and {b.dtype})")
     if b.shape[1] != K:
         raise ValueError(f"b must be [N, {K}] (got {tuple(b.shape)})")
-    op, ldo = _rows(out, "out", (M, N))
+    op, ldo = _rows(out, "out", dev, (M, N))
     kb = (K + 127) // 128
-    _call("veda_gemm_fp8", (a, a_scale, b, b_scale, bias, out), stream, M, N, K, ap, lda,
-          _ptr(a_scale, "a_scale", torch.float32, (kb, M)), bp, ldb,
-          _ptr(b_scale, "b_scale", torch.float32, ((N + 127) // 128, kb)), _ptr(bias, "bias", torch.float32, (N,)),
+    _call("veda_gemm_fp8", dev, stream, M, N, K, ap, lda, _at(a_scale, "a_scale", dev, _F32, (kb, M)), bp, ldb,
+          _at(b_scale, "b_scale", dev, _F32, ((N + 127) // 128, kb)), _at(bias, "bias", dev, _F32, (N,)),
           _type(out, "out"), op, ldo)
     return out
 
@@ -585,10 +608,11 @@ def veda_gemm_fp8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_sca
 def veda_rope_table(table: torch.Tensor, theta: float = 10000.0, start: float = 0.0, step: float = 1.0,
                     stream=None) -> torch.Tensor:
     """(cos, sin) of (start + step*i) * theta^(-2j/dim) into table [n, dim/2, 2] fp32 (angles in fp64)."""
+    dev = _device(table, "table")
     if table.dim() != 3 or table.shape[2] != 2:
         raise ValueError("table must be [n, dim/2, 2]")
-    _call("veda_rope_table", (table,), stream, table.shape[0], 2 * table.shape[1], theta, start, step,
-          _ptr(table, "table", torch.float32))
+    _call("veda_rope_table", dev, stream, table.shape[0], 2 * table.shape[1], theta, start, step,
+          _at(table, "table", dev, _F32, table.shape))
     return table
 
 
@@ -604,34 +628,36 @@ def make_rope(B: int, heads: int, d: int, grid: Sequence[int], tables: Sequence[
         raise ValueError("grid and tables have three entries: time, height, width")
     dims, ptrs = [], []
     for t, n in zip(tables, grid):
-        if t is not None and (t.dim() != 3 or t.shape[2] != 2 or t.shape[0] < n):
-            raise ValueError(f"a table must be [at least {n}, pairs, 2] (got {tuple(t.shape)})")
-        dims.append(0 if t is None else 2 * t.shape[1])
-        ptrs.append(None if t is None or t.shape[1] == 0 else _ptr(t, "table", torch.float32))
+        if t is None:
+            dims.append(0)
+            ptrs.append(None)
+            continue
+        shape = t.shape
+        if len(shape) != 3 or shape[2] != 2 or shape[0] < n:
+            raise ValueError(f"a table must be [at least {n}, pairs, 2] (got {tuple(shape)})")
+        dims.append(2 * shape[1])
+        ptrs.append(_at(t, "a table", _device(t, "a table"), _F32, shape) if shape[1] else None)
     return veda_rope(B, heads, d, veda_grid(*grid), *dims, *ptrs, _PAIRINGS[pairing], _NORMS[norm], eps)
 
 
-def _tokens(t: Optional[torch.Tensor], r: veda_rope, name: str, dtype: torch.dtype) -> Optional[veda_tokens]:
+def _tokens(t: Optional[torch.Tensor], r: veda_rope, name: str, dev: int, dtype: torch.dtype, shape):
+    """A token-order operand as the C struct's reference; shape: its [B, N, heads, d]."""
     if t is None:
         return None
-    n = r.grid.T * r.grid.H * r.grid.W
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if tuple(t.shape) != (r.B, n, r.heads, r.d) or t.stride(3) != 1 or t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype} [{r.B}, {n}, {r.heads}, {r.d}] with contiguous channels "
-                         f"(got {t.dtype} {tuple(t.shape)})")
-    return veda_tokens(t.data_ptr(), t.stride(0) if r.B > 1 else 0, t.stride(1) if n > 1 else 0,
-                       t.stride(2) if r.heads > 1 else 0)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the first operand on cuda:{dev}" if t.is_cuda
+                         else f"{name} must be a CUDA tensor")
+    sb, sn, sh, sc = t.stride() if t.dim() == 4 else (0, 0, 0, 0)
+    if t.shape != shape or sc != 1 or t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype} {list(shape)} with contiguous channels (got {t.dtype} {tuple(t.shape)})")
+    return ctypes.byref(veda_tokens(t.data_ptr(), sb if shape[0] > 1 else 0, sn if shape[1] > 1 else 0,
+                                    sh if shape[2] > 1 else 0))
 
 
-def _ref(s):
-    return None if s is None else ctypes.byref(s)
-
-
-def _norm_weight(w: Optional[torch.Tensor], r: veda_rope, name: str) -> Optional[int]:
-    if r.norm == 0 or w is None:
+def _norm_weight(w: Optional[torch.Tensor], r: veda_rope, name: str, dev: int) -> Optional[int]:
+    if w is None or r.norm == 0:
         return None
-    return _ptr(w, name, torch.float32, (r.heads * r.d if r.norm == 1 else r.d,))
+    return _at(w, name, dev, _F32, (r.heads * r.d if r.norm == 1 else r.d,))
 
 
 def _first(*ts):
@@ -645,20 +671,19 @@ def veda_qkv_norm_rope(r: veda_rope, q: Optional[torch.Tensor], k: Optional[torc
     some = _first(q, k, v)
     if some is None:
         raise ValueError("one of q, k and v is needed")
-    shape = (r.B, r.heads, r.grid.T * r.grid.H * r.grid.W, r.d)
-    tk = [_tokens(t, r, n, some.dtype) for t, n in ((q, "q"), (k, "k"), (v, "v"))]
-    _call("veda_qkv_norm_rope", (q, k, v, wq, wk, q_out, k_out, v_out), stream, ctypes.byref(r), _type(some, "q, k, v"),
-          _ref(tk[0]), _ref(tk[1]), _ref(tk[2]), _norm_weight(wq, r, "wq"), _norm_weight(wk, r, "wk"),
-          _ptr(q_out, "q_out", torch.bfloat16, shape), _ptr(k_out, "k_out", torch.bfloat16, shape),
-          _ptr(v_out, "v_out", torch.bfloat16, shape))
+    dev, dt, n = _device(some, "q, k, v"), some.dtype, r.grid.T * r.grid.H * r.grid.W
+    ins, outs = (r.B, n, r.heads, r.d), (r.B, r.heads, n, r.d)
+    _call("veda_qkv_norm_rope", dev, stream, ctypes.byref(r), _type(some, "q, k, v"), _tokens(q, r, "q", dev, dt, ins),
+          _tokens(k, r, "k", dev, dt, ins), _tokens(v, r, "v", dev, dt, ins), _norm_weight(wq, r, "wq", dev),
+          _norm_weight(wk, r, "wk", dev), _at(q_out, "q_out", dev, torch.bfloat16, outs),
+          _at(k_out, "k_out", dev, torch.bfloat16, outs), _at(v_out, "v_out", dev, torch.bfloat16, outs))
 
 
 def veda_qkv_norm_rope_backward_workspace(r: veda_rope, device=None) -> int:
     n = _SZ()
-    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    _on_device(dev, lambda: _check(LIB.veda_qkv_norm_rope_backward_workspace(ctypes.byref(r), ctypes.byref(n)),
-                                   "veda_qkv_norm_rope_backward_workspace"))
-    return int(n.value)
+    _on_device(device, lambda: _check(LIB.veda_qkv_norm_rope_backward_workspace(ctypes.byref(r), ctypes.byref(n)),
+                                      "veda_qkv_norm_rope_backward_workspace"))
+    return n.value
 
 
 def veda_qkv_norm_rope_backward(r: veda_rope, q: Optional[torch.Tensor], k: Optional[torch.Tensor],
@@ -671,14 +696,14 @@ def veda_qkv_norm_rope_backward(r: veda_rope, q: Optional[torch.Tensor], k: Opti
     some = _first(dq, dk, dv)
     if some is None:
         raise ValueError("one of dq, dk and dv is needed")
-    shape = (r.B, r.heads, r.grid.T * r.grid.H * r.grid.W, r.d)
-    tk = [_tokens(t, r, n, some.dtype) for t, n in ((q, "q"), (k, "k"), (dq, "dq"), (dk, "dk"), (dv, "dv"))]
-    _call("veda_qkv_norm_rope_backward", (q, k, wq, wk, d_q, d_k, d_v, dq, dk, dv, dwq, dwk, workspace), stream,
-          ctypes.byref(r), _type(some, "dq, dk, dv"), _ref(tk[0]), _ref(tk[1]), _norm_weight(wq, r, "wq"),
-          _norm_weight(wk, r, "wk"), _ptr(d_q, "d_q", torch.bfloat16, shape), _ptr(d_k, "d_k", torch.bfloat16, shape),
-          _ptr(d_v, "d_v", torch.bfloat16, shape), _ref(tk[2]), _ref(tk[3]), _ref(tk[4]),
-          _norm_weight(dwq, r, "dwq"), _norm_weight(dwk, r, "dwk"), _ptr(workspace, "workspace"),
-          0 if workspace is None else workspace.numel() * workspace.element_size())
+    dev, dt, n, bf = _device(some, "dq, dk, dv"), some.dtype, r.grid.T * r.grid.H * r.grid.W, torch.bfloat16
+    ins, outs = (r.B, n, r.heads, r.d), (r.B, r.heads, n, r.d)
+    _call("veda_qkv_norm_rope_backward", dev, stream, ctypes.byref(r), _type(some, "dq, dk, dv"),
+          _tokens(q, r, "q", dev, dt, ins), _tokens(k, r, "k", dev, dt, ins), _norm_weight(wq, r, "wq", dev),
+          _norm_weight(wk, r, "wk", dev), _at(d_q, "d_q", dev, bf, outs), _at(d_k, "d_k", dev, bf, outs),
+          _at(d_v, "d_v", dev, bf, outs), _tokens(dq, r, "dq", dev, dt, ins), _tokens(dk, r, "dk", dev, dt, ins),
+          _tokens(dv, r, "dv", dev, dt, ins), _norm_weight(dwq, r, "dwq", dev), _norm_weight(dwk, r, "dwk", dev),
+          *_scratch(workspace, dev))
 
 
 def veda_sync_status(stream=None) -> None:

@@ -168,12 +168,34 @@ struct NormBwdArgs {
   const float *w, *rstd;
   void *dx, *ddelta;   // either may be null
   float* part;         // [parts, C] or null
+  float* dw;
   int parts, warps;
 };
 
+// Sums of partial rows: out[i][c] = sum_p part[i][p, c].
+struct SumArgs {
+  const float* part[2];
+  float* out[2];
+  int parts, C;
+};
+constexpr int kBwdCtasPerSm = 3;   // of the kernels that write partial rows
+
+// n / d for 0 <= n < 2^31 by one multiplication.
+struct FastDiv {
+  uint32_t d, mul, shift;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t divisor) : d(divisor), shift(0) {
+    while ((1ull << shift) < d) ++shift;
+    mul = (uint32_t)((((1ull << shift) - d) << 32) / d + 1);
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
+};
+
 struct RopeArgs {
-  int heads, d, H, W, N;
-  long long tokens;             // B * N
+  int heads, d, H, W, HW, N;
+  long long tokens;             // B * N, below 2^31
+  FastDiv by_n, by_hw, by_w;
+  float inv_n;                  // 1 / the channels of a norm
   int norm, halves;
   float eps;
   int dim[3];
@@ -184,8 +206,9 @@ struct RopeArgs {
   void* dx[3];                  // backward
   long long sb[3], sn[3], sh[3], dsb[3], dsn[3], dsh[3];   // element strides of in and dx
   float* part[3];
+  float* dw[2];
   int parts, warps;
-  int order[3];                 // the operands of this launch: 0 Q, 1 K, 2 V
+  int order[3], n_order;        // the operands of this launch: 0 Q, 1 K, 2 V
 };
 
 struct QuantArgs {
@@ -208,12 +231,11 @@ struct GemmArgs {
 
 cudaError_t launch_add_rms_norm(NormArgs a, int tx, int td, bool fp8, int sms, cudaStream_t s);
 int add_rms_norm_bwd_parts(long long rows, int C, int sms);
-cudaError_t launch_add_rms_norm_bwd(NormBwdArgs a, int tx, int td, float* dw, int sms, cudaStream_t s);
-cudaError_t launch_sum_partials(const float* part, int parts, int C, float* out, cudaStream_t s);
+cudaError_t launch_add_rms_norm_bwd(NormBwdArgs a, int tx, int td, int sms, cudaStream_t s);
+cudaError_t launch_sum_partials(const SumArgs& a, int n, cudaStream_t s);
 
-cudaError_t launch_qkv_rope(RopeArgs a, int type, int n_which, int sms, cudaStream_t s);
-int qkv_rope_bwd_parts(long long tokens, int heads, int d, bool row, int sms);
-cudaError_t launch_qkv_rope_bwd(RopeArgs a, int type, int n_which, float* const* dw, int sms, cudaStream_t s);
+cudaError_t launch_qkv_rope(RopeArgs a, int type, bool backward, int sms, cudaStream_t s);
+int qkv_rope_bwd_parts(long long tokens, int heads, int d, int sms);
 cudaError_t launch_rope_table(int n, int dim, double theta, double start, double step, float* out, cudaStream_t s);
 
 cudaError_t launch_quant_rows(const QuantArgs& a, int type, cudaStream_t s);

@@ -61,6 +61,7 @@ veda_status make_rope(const veda_rope* r, RopeArgs* a) {
   const long long hw = (long long)r->grid.H * r->grid.W;
   if (hw > (1LL << 30) || hw * r->grid.T > (1LL << 30)) return fail(VEDA_ERR_INVALID_ARG, "grid has too many tokens");
   const long long N = hw * r->grid.T;
+  if (N * r->B >= (1LL << 31)) return fail(VEDA_ERR_INVALID_ARG, "B x the grid exceeds 2^31 tokens");
   if (r->norm != VEDA_NORM_NONE && r->norm != VEDA_NORM_ROW && r->norm != VEDA_NORM_HEAD)
     return fail(VEDA_ERR_INVALID_ARG, "unknown norm %d", (int)r->norm);
   if (r->pairing != VEDA_PAIR_INTERLEAVED && r->pairing != VEDA_PAIR_HALVES)
@@ -108,7 +109,7 @@ size_t rope_part_bytes(const RopeArgs& a) {
   if (a.norm == VEDA_NORM_NONE) return 0;
   const bool row = a.norm == VEDA_NORM_ROW;
   const size_t C = row ? (size_t)a.heads * a.d : (size_t)a.d;
-  return round256(sizeof(float) * C * qkv_rope_bwd_parts(a.tokens, a.heads, a.d, row, sm_count()));
+  return round256(sizeof(float) * C * qkv_rope_bwd_parts(a.tokens, a.heads, a.d, sm_count()));
 }
 
 // 2D view [rows, K] of an e4m3 operand, boxes of 128 channels x box_rows rows,
@@ -189,7 +190,8 @@ veda_status veda_add_rms_norm_backward(int64_t rows, int32_t C, veda_dtype x_typ
   a.dx = dx;
   a.ddelta = ddelta;
   a.part = dweight ? static_cast<float*>(workspace) : nullptr;
-  const cudaError_t e = launch_add_rms_norm_bwd(a, x_type, delta_type, dweight, sm_count(), (cudaStream_t)stream);
+  a.dw = dweight;
+  const cudaError_t e = launch_add_rms_norm_bwd(a, x_type, delta_type, sm_count(), (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "veda_add_rms_norm_backward");
   return ok();
 }
@@ -324,7 +326,8 @@ veda_status veda_qkv_norm_rope(const veda_rope* r, veda_dtype type, const veda_t
     a.order[n++] = i;
   }
   if (n == 0) return fail(VEDA_ERR_INVALID_ARG, "no operand is given");
-  const cudaError_t e = launch_qkv_rope(a, type, n, sm_count(), (cudaStream_t)stream);
+  a.n_order = n;
+  const cudaError_t e = launch_qkv_rope(a, type, false, sm_count(), (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "veda_qkv_norm_rope");
   return ok();
 }
@@ -378,6 +381,7 @@ veda_status veda_qkv_norm_rope_backward(const veda_rope* r, veda_dtype type, con
       a.w[i] = w[i];
       if (dw[i]) {
         a.part[i] = reinterpret_cast<float*>(static_cast<char*>(workspace) + (i ? part : 0));
+        a.dw[i] = dw[i];
         needs_part = true;
       }
     }
@@ -392,7 +396,8 @@ veda_status veda_qkv_norm_rope_backward(const veda_rope* r, veda_dtype type, con
   if (needs_part && (!workspace || !aligned16(workspace) || workspace_bytes < 2 * part))
     return fail(VEDA_ERR_INVALID_ARG, "workspace of %zu bytes, 16-byte aligned, is needed (got %zu)", 2 * part,
                 workspace ? workspace_bytes : 0);
-  const cudaError_t e = launch_qkv_rope_bwd(a, type, n, dw, sm_count(), (cudaStream_t)stream);
+  a.n_order = n;
+  const cudaError_t e = launch_qkv_rope(a, type, true, sm_count(), (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "veda_qkv_norm_rope_backward");
   return ok();
 }

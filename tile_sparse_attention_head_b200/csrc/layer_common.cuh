@@ -46,6 +46,44 @@ __device__ __forceinline__ void load8<__half>(const __half* p, float* v) {
   }
 }
 
+// Chunks on their way from global memory, D rows ahead of their use, in shared
+// memory.  A thread copies (cp.async, 16 bytes at a time) and reads its own
+// chunks only, so nothing has to be synchronised between threads: one commit
+// per row, and a wait for all but the D - 1 newest rows before reading.  The
+// layout is [slot][chunk][16-byte piece][thread]: no bank conflicts.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <typename T, int CPT>
+struct Ring {
+  static constexpr int kPieces = sizeof(T) / 2;
+  static constexpr int kBytes = CPT * kPieces * 16;   // per thread and slot
+  const uint4* base;
+  __device__ __forceinline__ explicit Ring(const void* smem) : base(static_cast<const uint4*>(smem) + threadIdx.x) {}
+  __device__ __forceinline__ const uint4* at(int slot, int i, int k) const {
+    return base + ((slot * CPT + i) * kPieces + k) * blockDim.x;
+  }
+  __device__ __forceinline__ void fetch(int slot, int i, const T* p) const {
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) cp_async16(smem_u32(at(slot, i, k)), reinterpret_cast<const uint4*>(p) + k);
+  }
+  __device__ __forceinline__ void read(int slot, int i, float* v) const {
+    uint4 u[kPieces];
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) u[k] = *at(slot, i, k);
+    load8(reinterpret_cast<const T*>(u), v);
+  }
+};
+
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const float* v);
 template <>
@@ -83,15 +121,81 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Sum over the `warps` warps of the CTA, the same value in every thread (the
-// addition order is fixed).  `red` holds 2 x 32 floats; `turn` alternates
-// between calls, so one barrier per call is enough: a warp can only be one
+// How rows are spread over threads: a row belongs to `W` warps of a CTA (its
+// group), `cpt` chunks per thread, and a CTA has up to as many groups as make
+// 16 warps.  Thread t of a group has the chunks t, t + 32 W, ...
+struct RowSplit {
+  int cpt, W, groups, threads;
+};
+inline RowSplit row_split(int nchunk, long long rows, int sms) {
+  RowSplit r;
+  r.cpt = nchunk <= 32 ? 1 : nchunk <= 1024 ? 2 : 4;
+  r.W = (nchunk + 32 * r.cpt - 1) / (32 * r.cpt);
+  r.groups = 16 / r.W;
+  const long long each = (rows + sms - 1) / sms;   // few rows: spread them over the SMs first
+  if (each < r.groups) r.groups = each < 1 ? 1 : (int)each;
+  r.threads = 32 * r.W * r.groups;
+  return r;
+}
+
+struct RowGroup {
+  int W, groups, group, warp, lane, t, tpt;   // warp: within the group
+  __device__ __forceinline__ explicit RowGroup(int warps) {
+    W = warps;
+    groups = (int)(blockDim.x >> 5) / W;
+    const int w = threadIdx.x >> 5;
+    group = w / W;
+    warp = w - group * W;
+    lane = threadIdx.x & 31;
+    t = warp * 32 + lane;
+    tpt = 32 * W;
+  }
+};
+
+__device__ __forceinline__ void group_sync(const RowGroup& g) {
+  if (g.W == 1) __syncwarp();
+  else asm volatile("bar.sync %0, %1;" ::"r"(g.group + 1), "r"(32 * g.W) : "memory");
+}
+
+// Sums over the threads of a group, the same in every thread (the addition
+// order is fixed).  `red` holds kRowRed floats per CTA; `turn` alternates
+// between calls, so that one barrier per call is enough: a warp can only be one
 // call ahead of the slowest reader.
-__device__ __forceinline__ float cta_sum(float v, float* red, int warps, int warp, int lane, int turn) {
-  v = warp_sum(v);
-  if (lane == 0) red[turn * 32 + warp] = v;
-  __syncthreads();
-  return warp_sum(lane < warps ? red[turn * 32 + lane] : 0.f);
+constexpr int kRowRed = 16 * 2 * 2 * 16;
+__device__ __forceinline__ void row_sum2(const RowGroup& g, float& a, float& b, float* red, int turn) {
+  a = warp_sum(a);
+  b = warp_sum(b);
+  if (g.W == 1) return;
+  float* r = red + (g.group * 2 + turn) * 32;
+  if (g.lane == 0) {
+    r[g.warp] = a;
+    r[16 + g.warp] = b;
+  }
+  group_sync(g);
+  a = warp_sum(g.lane < g.W ? r[g.lane] : 0.f);
+  b = warp_sum(g.lane < g.W ? r[16 + g.lane] : 0.f);
+}
+__device__ __forceinline__ float row_sum(const RowGroup& g, float a, float* red, int turn) {
+  a = warp_sum(a);
+  if (g.W == 1) return a;
+  float* r = red + (g.group * 2 + turn) * 32;
+  if (g.lane == 0) r[g.warp] = a;
+  group_sync(g);
+  return warp_sum(g.lane < g.W ? r[g.lane] : 0.f);
+}
+
+template <typename K>
+inline cudaError_t allow_smem(K kernel, size_t smem) {
+  if (smem <= 40 * 1024) return cudaSuccess;   // what any kernel may have beside its static part
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+}
+
+// CTAs that are resident at once, so that each can keep stepping over rows.
+template <typename K>
+inline unsigned resident_ctas(K kernel, int threads, size_t smem, int sms) {
+  int n = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess || n < 1) n = 1;
+  return (unsigned)(n * sms);
 }
 
 // The 8-bit rule: a block's scale is s = a / 448 with a its largest magnitude,

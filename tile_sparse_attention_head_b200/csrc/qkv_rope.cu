@@ -15,12 +15,15 @@
 // rstd is recomputed from x, which backward reads anyway.  Everything between
 // the loads and the one rounding at the store is fp32.
 //
-// HBM is the bound: each element is read once and written once.  A thread owns
-// chunks of 8 channels; chunk c of a token belongs to thread c % tpt with tpt
-// a multiple of 32, hence of d/8, so a thread meets the same channels of a
-// head in all its chunks and fetches its cos and sin once per token.  Stores to
-// grid order are whole head rows (128 or 256 bytes).  Tokens of up to 1,024
-// channels take a warp each, longer ones a CTA of as many warps as they need.
+// HBM is the bound: each element is read once and written once.  A token's row
+// of one operand belongs to a group of warps (as in the norm), which steps over
+// the tokens with the next rows on their way to shared memory, first all of Q,
+// then K, then V, so that the operand's weights and angle addresses stay in
+// registers.  Chunk c of a row belongs to thread c % tpt with tpt a multiple of
+// 32, hence of d/8, so a thread meets the same channels of a head in all its
+// chunks and reads its cos and sin once per token.  A token's d/2 angles come
+// to shared memory with its row, one copy for the group.  Stores to grid order
+// are whole head rows (128 or 256 bytes).
 #include "layer_common.cuh"
 #include "kernels.h"
 #undef VEDA_SRC_ID
@@ -28,71 +31,118 @@
 
 namespace veda {
 
-// Where the angle of channel `ch` of a head comes from.
-struct Angle {
-  int axis;      // 0 time, 1 height, 2 width, -1 not turned
-  int at;        // column of the axis's table
-  int partner;   // the pair's other channel
-  bool second;   // whether ch is the pair's second channel
+// A channel's pair and its place in it; pair p has column p - base / 2 of its
+// axis's table (base: the axis's first channel) in both pairings.
+struct PairOf {
+  int pair, partner;
+  bool second, turned;
 };
-
-__device__ __forceinline__ Angle angle_of(const RopeArgs& A, int ch) {
-  Angle g{-1, 0, ch, false};
+__device__ __forceinline__ PairOf pair_of(const RopeArgs& A, int ch) {
+  PairOf g{0, ch, false, false};
   int base = 0;
 #pragma unroll
   for (int a = 0; a < 3; ++a) {
-    const int u = ch - base, dim = A.dim[a];
+    const int u = ch - base, dim = A.dim[a], half = dim >> 1;
     if (u >= 0 && u < dim) {
-      g.axis = a;
-      if (A.halves) {
-        const int half = dim >> 1;
-        g.second = u >= half;
-        g.at = g.second ? u - half : u;
-        g.partner = g.second ? ch - half : ch + half;
-      } else {
-        g.second = u & 1;
-        g.at = u >> 1;
-        g.partner = ch ^ 1;
-      }
+      g.turned = true;
+      g.second = A.halves ? u >= half : (u & 1);
+      g.pair = (base >> 1) + (A.halves ? (g.second ? u - half : u) : u >> 1);
+      g.partner = A.halves ? (g.second ? ch - half : ch + half) : ch ^ 1;
     }
     base += dim;
   }
   return g;
 }
 
-// Per-thread addresses of the angles of its 8 channels: HALVES needs one angle
-// per channel, neighbours share one.
-template <bool HALVES>
-struct Turn {
-  static constexpr int kN = HALVES ? 8 : 4;
-  const float2* base[kN];
-  int step[kN];       // table row length, 0 where the channel is not turned
-  int axis[kN];
-  int src[HALVES ? 8 : 1];     // partner's place in the warp's scratch
-  float sgn[HALVES ? 8 : 1];
-  __device__ __forceinline__ void init(const RopeArgs& A, int ch0, int lane, int lanes_per_head) {
+// Place of a token: batch, index in the grid, and the grid's coordinates.
+struct Place {
+  int b, n, t, y, x;
+  __device__ __forceinline__ Place(const RopeArgs& A, int tok) {
+    b = A.by_n.div(tok);
+    n = tok - b * A.N;
+    t = A.by_hw.div(n);
+    const int r = n - t * A.HW;
+    y = A.by_w.div(r);
+    x = r - y * A.W;
+  }
+};
+
+// The angles of the group's tokens in shared memory: kSlots = D + 2 rows of up
+// to 64 (cos, sin).  Row r + D is fetched in iteration r over row r - 2, which
+// every thread of the group has left: all of them have met at a barrier of
+// iteration r - 1.
+template <bool HALVES, int D>
+struct Angles {
+  static constexpr int kSlots = D + 2;
+  static constexpr int kRow = HALVES ? 72 : 64;   // padded by one per 8 pairs where threads read with a stride
+  static constexpr size_t kBytes = kSlots * kRow * sizeof(float2);
+  static constexpr int kN = HALVES ? 8 : 4;       // angles per chunk
+  float2* rows;
+  // What this thread fetches: the pairs t and t + tpt (the second for d = 128 in one warp).
+  const float2* src[2];
+  int step[2], axis[2];
+  // What it reads: bit j of `turned` for the pair of channel j (halves) or 2j, 2j + 1; and for
+  // halves the pair's place, the partner's place in the warp's scratch, and whether it is the second.
+  uint32_t turned;
+  uint32_t at[HALVES ? 8 : 1];
+  __device__ __forceinline__ static int place(int pair) { return HALVES ? pair + (pair >> 3) : pair; }
+  __device__ __forceinline__ Angles(const RopeArgs& A, void* smem, const RowGroup& g, int ch0, int lph) {
+    rows = static_cast<float2*>(smem) + g.group * (kSlots * kRow);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int pair = g.t + j * g.tpt;
+      src[j] = nullptr;
+      step[j] = axis[j] = 0;
+      int base = 0;
+#pragma unroll
+      for (int a = 0; a < 3; ++a) {
+        const int n = A.dim[a] >> 1;
+        if (pair >= base && pair < base + n) {
+          src[j] = A.tab[a] + (pair - base);
+          step[j] = n;
+          axis[j] = a;
+        }
+        base += n;
+      }
+    }
+    turned = 0;
 #pragma unroll
     for (int j = 0; j < kN; ++j) {
-      const Angle g = angle_of(A, ch0 + (HALVES ? j : 2 * j));
-      axis[j] = g.axis;
-      step[j] = g.axis < 0 ? 0 : A.dim[g.axis] >> 1;
-      base[j] = g.axis < 0 ? nullptr : A.tab[g.axis] + g.at;
+      const PairOf p = pair_of(A, ch0 + (HALVES ? j : 2 * j));
+      turned |= (p.turned ? 1u : 0u) << j;
       if constexpr (HALVES) {
-        const int first = lane / lanes_per_head * lanes_per_head;
-        src[j] = (first + (g.partner >> 3)) * 9 + (g.partner & 7);
-        sgn[j] = g.second ? 1.f : -1.f;
+        const int first = g.lane / lph * lph;
+        at[j] = (uint32_t)place(p.pair) | (uint32_t)((first + (p.partner >> 3)) * 9 + (p.partner & 7)) << 8 |
+                (p.second ? 1u << 31 : 0u);
       }
     }
   }
-  __device__ __forceinline__ void load(int t, int y, int x, float2* cs) const {
+  __device__ __forceinline__ void fetch(const RowGroup& g, int slot, const Place& p) const {
 #pragma unroll
-    for (int j = 0; j < kN; ++j) {
-      const int pos = axis[j] == 0 ? t : axis[j] == 1 ? y : x;
-      cs[j] = axis[j] < 0 ? make_float2(1.f, 0.f) : base[j][pos * step[j]];
+    for (int j = 0; j < 2; ++j) {
+      if (src[j] != nullptr) {
+        const int pos = axis[j] == 0 ? p.t : axis[j] == 1 ? p.y : p.x;
+        cp_async8(smem_u32(rows + slot * kRow + place(g.t + j * g.tpt)), src[j] + (long long)pos * step[j]);
+      }
     }
   }
-  // v turned by +angle (dir = 1) or -angle (dir = -1).  `scratch`: this
-  // warp's 32 * 9 floats (a lane's 8 values at 9 * lane: no bank conflicts).
+  __device__ __forceinline__ void read(int slot, int ch0, float2* cs) const {
+    const float2* r = rows + slot * kRow;
+    if constexpr (HALVES) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) cs[j] = r[at[j] & 0xff];
+    } else {
+      const float4* q = reinterpret_cast<const float4*>(r + (ch0 >> 1));
+      const float4 a = q[0], b = q[1];
+      cs[0] = make_float2(a.x, a.y);
+      cs[1] = make_float2(a.z, a.w);
+      cs[2] = make_float2(b.x, b.y);
+      cs[3] = make_float2(b.z, b.w);
+    }
+  }
+  // v turned by +angle (dir = 1) or -angle (dir = -1); a channel that is not
+  // turned stays as it is, an infinity too.  `scratch`: this warp's 32 * 9
+  // floats (a lane's 8 values at 9 * lane: no bank conflicts).
   __device__ __forceinline__ void apply(float* v, const float2* cs, float dir, float* scratch, int lane) const {
     if constexpr (HALVES) {
       __syncwarp();
@@ -101,15 +151,17 @@ struct Turn {
       __syncwarp();
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float r = fmaf(v[j], cs[j].x, sgn[j] * dir * cs[j].y * scratch[src[j]]);
-        v[j] = axis[j] < 0 ? v[j] : r;   // an infinity that is not turned stays one
+        const float s = (at[j] >> 31 ? dir : -dir) * cs[j].y;
+        const float r = fmaf(v[j], cs[j].x, s * scratch[(at[j] >> 8) & 0x1ff]);
+        v[j] = turned >> j & 1 ? r : v[j];
       }
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float a = v[2 * j], b = v[2 * j + 1], s = dir * cs[j].y;
-        v[2 * j] = axis[j] < 0 ? a : fmaf(a, cs[j].x, -b * s);
-        v[2 * j + 1] = axis[j] < 0 ? b : fmaf(a, s, b * cs[j].x);
+        const bool on = turned >> j & 1;
+        v[2 * j] = on ? fmaf(a, cs[j].x, -b * s) : a;
+        v[2 * j + 1] = on ? fmaf(a, s, b * cs[j].x) : b;
       }
     }
   }
@@ -120,210 +172,253 @@ __device__ __forceinline__ float head_sum(float v, int lanes) {
   return v;
 }
 
-// A.order[blockIdx.y]: 0 = Q, 1 = K, 2 = V (V is only moved).
+// Rows in flight per group, and the thread count that register use is bounded
+// by: two CTAs of up to 10 warps (or of 512 threads with one chunk each) are to
+// fit an SM.
+__host__ __device__ constexpr int rope_bounds(int cpt) { return cpt == 1 ? 1024 : cpt == 2 ? 640 : 512; }
+__host__ __device__ constexpr int rope_depth(int cpt) { return cpt == 4 ? 2 : 4; }
+__host__ __device__ constexpr int rope_bwd_depth(int cpt) { return cpt == 4 ? 1 : 3; }
+
 template <typename T, int CPT, bool HALVES>
-__global__ void __launch_bounds__(512) qkv_rope_kernel(const __grid_constant__ RopeArgs A) {
-  __shared__ float red[64];
-  extern __shared__ float scratch_all[];
-  const int which = A.order[blockIdx.y];
-  const int W = A.warps, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per_cta = W == 1 ? (int)(blockDim.x >> 5) : 1;
-  const int t = W == 1 ? lane : threadIdx.x;
-  const int tpt = 32 * W, lph = A.d / 8, nchunk = A.heads * lph;
-  const int ch0 = (t % lph) * 8, head0 = t / lph, head_step = tpt / lph;
-  const int norm = which == 2 ? VEDA_NORM_NONE : A.norm;
-  const T* in = static_cast<const T*>(A.in[which]);
-  const long long sb = A.sb[which], sn = A.sn[which], sh = A.sh[which];
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(A.out[which]);
-  float* scratch = scratch_all + warp * (32 * 9);
-  Turn<HALVES> turn;
-  turn.init(A, ch0, lane, lph);
-  float w[CPT][8];
-#pragma unroll
-  for (int i = 0; i < CPT; ++i) {
-    const int c = t + i * tpt;
-    if (norm != VEDA_NORM_NONE && c < nchunk) load8(A.w[which] + (norm == VEDA_NORM_ROW ? 8 * c : ch0), w[i]);
-  }
-  const float inv_n = 1.f / (float)(norm == VEDA_NORM_ROW ? A.heads * A.d : A.d);
+__global__ void __launch_bounds__(rope_bounds(CPT)) qkv_rope_kernel(const __grid_constant__ RopeArgs A) {
+  constexpr int D = rope_depth(CPT);
+  __shared__ float red[kRowRed];
+  extern __shared__ uint4 ring_raw[];
+  const RowGroup g(A.warps);
+  const Ring<T, CPT> ring(ring_raw);
+  uint8_t* rest = reinterpret_cast<uint8_t*>(ring_raw) + D * Ring<T, CPT>::kBytes * blockDim.x;
+  float* scratch = reinterpret_cast<float*>(rest + g.groups * Angles<HALVES, D>::kBytes) + (threadIdx.x >> 5) * (32 * 9);
+  const int lph = A.d / 8, nchunk = A.heads * lph;
+  const int ch0 = (g.t % lph) * 8, head0 = g.t / lph, head_step = g.tpt / lph;
+  const int step = gridDim.x * g.groups, first = blockIdx.x * g.groups + g.group;
+  const Angles<HALVES, D> angles(A, rest, g, ch0, lph);
   int flip = 0;
-  for (long long tok = (long long)blockIdx.x * per_cta + (W == 1 ? warp : 0); tok < A.tokens;
-       tok += (long long)gridDim.x * per_cta, flip ^= 1) {
-    const int b = (int)(tok / A.N), n = (int)(tok % A.N);
-    const T* row = in + b * sb + n * sn;
-    float v[CPT][8];
-    float r[CPT];
-    float ss = 0.f;
+  for (int o = 0; o < A.n_order; ++o) {
+    if (o > 0) __syncthreads();   // the angles' slots start over
+    const int which = A.order[o];
+    const int norm = which == 2 ? VEDA_NORM_NONE : A.norm;
+    const T* in = static_cast<const T*>(A.in[which]) + ch0;
+    const long long sb = A.sb[which], sn = A.sn[which], sh = A.sh[which];
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(A.out[which]) + ch0;
+    auto fetch = [&](int tok, int slot, int aslot) {
+      if (tok < A.tokens) {
+        const Place at(A, tok);
+        if (which < 2) angles.fetch(g, aslot, at);
+        const T* row = in + at.b * sb + at.n * sn;
+#pragma unroll
+        for (int i = 0; i < CPT; ++i)
+          if (g.t + i * g.tpt < nchunk) ring.fetch(slot, i, row + (head0 + i * head_step) * sh);
+      }
+      cp_async_commit();
+    };
+#pragma unroll 1
+    for (int s = 0; s < D; ++s) fetch(first + s * step, s, s);
+    float w[CPT][8];
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
-      const int c = t + i * tpt;
-      if (c < nchunk && VEDA_IN_BOUNDS(tok < A.tokens)) {
-        load8(row + (head0 + i * head_step) * sh + ch0, v[i]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[i][k] = 0.f;
-      }
+      const int c = g.t + i * g.tpt;
+      if (norm != VEDA_NORM_NONE && c < nchunk) load8(A.w[which] + (norm == VEDA_NORM_ROW ? 8 * c : ch0), w[i]);
     }
-    float2 cs[Turn<HALVES>::kN];
-    if (which < 2) turn.load(n / (A.H * A.W), n / A.W % A.H, n % A.W, cs);
-    if (norm != VEDA_NORM_NONE) {
+    int slot = 0, aslot = 0;
+    auto next = [](int s, int n) { return s + 1 == n ? 0 : s + 1; };
+    for (int tok = first; tok < A.tokens; tok += step, flip ^= 1, slot = next(slot, D), aslot = next(aslot, D + 2)) {
+      const int b = A.by_n.div(tok), n = tok - b * A.N;
+      float v[CPT][8];
+      cp_async_wait<D - 1>();
 #pragma unroll
       for (int i = 0; i < CPT; ++i) {
-        float s = 0.f;
+        ring.read(slot, i, v[i]);
+        if (g.t + i * g.tpt >= nchunk) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) s = fmaf(v[i][k], v[i][k], s);
-        r[i] = s;
-        ss += s;
+          for (int k = 0; k < 8; ++k) v[i][k] = 0.f;
+        }
       }
-      if (norm == VEDA_NORM_ROW) {
-        ss = W == 1 ? warp_sum(ss) : cta_sum(ss, red, W, warp, lane, flip);
-        ss = rsqrtf(ss * inv_n + A.eps);
+      fetch(tok + D * step, slot, aslot >= 2 ? aslot - 2 : aslot + D);
+      if (g.W == 1 || (which < 2 && norm != VEDA_NORM_ROW)) group_sync(g);   // a row's sum is a barrier itself
+      if (norm != VEDA_NORM_NONE) {
+        float r[CPT];
+        float ss = 0.f;
 #pragma unroll
-        for (int i = 0; i < CPT; ++i) r[i] = ss;
-      } else {
+        for (int i = 0; i < CPT; ++i) {
+          r[i] = 0.f;
 #pragma unroll
-        for (int i = 0; i < CPT; ++i) r[i] = rsqrtf(head_sum(r[i], lph) * inv_n + A.eps);
+          for (int k = 0; k < 8; ++k) r[i] = fmaf(v[i][k], v[i][k], r[i]);
+          ss += r[i];
+        }
+        if (norm == VEDA_NORM_ROW) {
+          ss = rsqrtf(row_sum(g, ss, red, flip) * A.inv_n + A.eps);
+#pragma unroll
+          for (int i = 0; i < CPT; ++i) r[i] = ss;
+        } else {
+#pragma unroll
+          for (int i = 0; i < CPT; ++i) r[i] = rsqrtf(head_sum(r[i], lph) * A.inv_n + A.eps);
+        }
+#pragma unroll
+        for (int i = 0; i < CPT; ++i) {
+          if (g.t + i * g.tpt < nchunk) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[i][k] *= r[i] * w[i][k];
+          }
+        }
       }
-    }
+      const long long row = (long long)b * A.heads * A.N + n;
+      float2 cs[Angles<HALVES, D>::kN];
+      if (which < 2) angles.read(aslot, ch0, cs);
 #pragma unroll
-    for (int i = 0; i < CPT; ++i) {
-      const int c = t + i * tpt;
-      if (norm != VEDA_NORM_NONE && c < nchunk) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[i][k] *= r[i] * w[i][k];
+      for (int i = 0; i < CPT; ++i) {
+        const int head = head0 + i * head_step;
+        if (which < 2) angles.apply(v[i], cs, 1.f, scratch, g.lane);
+        if (g.t + i * g.tpt < nchunk && VEDA_IN_BOUNDS(head < A.heads && tok < A.tokens))
+          store8(out + (row + (long long)head * A.N) * A.d, v[i]);
       }
-      if (which < 2) turn.apply(v[i], cs, 1.f, scratch, lane);
-      if (c < nchunk && VEDA_IN_BOUNDS(head0 + i * head_step < A.heads))
-        store8(out + (((long long)b * A.heads + head0 + i * head_step) * A.N + n) * A.d + ch0, v[i]);
     }
   }
 }
 
 template <typename T, int CPT, bool HALVES>
 __global__ void __launch_bounds__(512) qkv_rope_bwd_kernel(const __grid_constant__ RopeArgs A) {
-  __shared__ float red[64];
-  extern __shared__ float scratch_all[];
-  const int which = A.order[blockIdx.y];
-  const int W = A.warps, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per_cta = W == 1 ? (int)(blockDim.x >> 5) : 1;
-  const int t = W == 1 ? lane : threadIdx.x;
-  const int tpt = 32 * W, lph = A.d / 8, nchunk = A.heads * lph;
-  const int ch0 = (t % lph) * 8, head0 = t / lph, head_step = tpt / lph;
-  const int norm = which == 2 ? VEDA_NORM_NONE : A.norm;
-  const T* in = static_cast<const T*>(A.in[which]);
-  const long long sb = A.sb[which], sn = A.sn[which], sh = A.sh[which];
-  const __nv_bfloat16* dout = static_cast<const __nv_bfloat16*>(A.out[which]);
-  T* dx = static_cast<T*>(A.dx[which]);
-  const long long dsb = A.dsb[which], dsn = A.dsn[which], dsh = A.dsh[which];
-  float* scratch = scratch_all + warp * (32 * 9);
-  Turn<HALVES> turn;
-  turn.init(A, ch0, lane, lph);
-  float w[CPT][8], acc[CPT][8];
+  constexpr int D = rope_bwd_depth(CPT);
+  __shared__ float red[kRowRed];
+  extern __shared__ uint4 ring_raw[];
+  const RowGroup g(A.warps);
+  const Ring<T, CPT> rx(ring_raw);
+  const Ring<__nv_bfloat16, CPT> rg(ring_raw + D * Ring<T, CPT>::kBytes / 16 * blockDim.x);
+  uint8_t* rest = reinterpret_cast<uint8_t*>(ring_raw) +
+                  D * (Ring<T, CPT>::kBytes + Ring<__nv_bfloat16, CPT>::kBytes) * blockDim.x;
+  float* scratch = reinterpret_cast<float*>(rest + g.groups * Angles<HALVES, D>::kBytes) + (threadIdx.x >> 5) * (32 * 9);
+  const int lph = A.d / 8, nchunk = A.heads * lph;
+  const int ch0 = (g.t % lph) * 8, head0 = g.t / lph, head_step = g.tpt / lph;
+  const int step = gridDim.x * g.groups, first = blockIdx.x * g.groups + g.group;
+  const Angles<HALVES, D> angles(A, rest, g, ch0, lph);
+  int flip = 0;
+  for (int o = 0; o < A.n_order; ++o) {
+    if (o > 0) __syncthreads();   // the angles' slots start over
+    const int which = A.order[o];
+    const int norm = which == 2 ? VEDA_NORM_NONE : A.norm;
+    const T* in = static_cast<const T*>(A.in[which]) + ch0;
+    const long long sb = A.sb[which], sn = A.sn[which], sh = A.sh[which];
+    const __nv_bfloat16* dout = static_cast<const __nv_bfloat16*>(A.out[which]) + ch0;
+    T* dx = static_cast<T*>(A.dx[which]) + ch0;
+    const long long dsb = A.dsb[which], dsn = A.dsn[which], dsh = A.dsh[which];
+    auto fetch = [&](int tok, int slot, int aslot) {
+      if (tok < A.tokens) {
+        const Place at(A, tok);
+        if (which < 2) angles.fetch(g, aslot, at);
+        const long long row = (long long)at.b * A.heads * A.N + at.n;
 #pragma unroll
-  for (int i = 0; i < CPT; ++i) {
-    const int c = t + i * tpt;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) acc[i][k] = w[i][k] = 0.f;
-    if (norm != VEDA_NORM_NONE && c < nchunk) load8(A.w[which] + (norm == VEDA_NORM_ROW ? 8 * c : ch0), w[i]);
-  }
-  const float inv_n = 1.f / (float)(norm == VEDA_NORM_ROW ? A.heads * A.d : A.d);
-  for (long long tok = (long long)blockIdx.x * per_cta + (W == 1 ? warp : 0); tok < A.tokens;
-       tok += (long long)gridDim.x * per_cta) {
-    const int b = (int)(tok / A.N), n = (int)(tok % A.N);
-    float g[CPT][8], v[CPT][8];
-#pragma unroll
-    for (int i = 0; i < CPT; ++i) {
-      const int c = t + i * tpt, hd = head0 + i * head_step;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) g[i][k] = v[i][k] = 0.f;
-      if (c < nchunk && VEDA_IN_BOUNDS(hd < A.heads)) {
-        load8(dout + (((long long)b * A.heads + hd) * A.N + n) * A.d + ch0, g[i]);
-        if (norm != VEDA_NORM_NONE) load8(in + b * sb + n * sn + hd * sh + ch0, v[i]);
-      }
-    }
-    if (which < 2) {
-      float2 cs[Turn<HALVES>::kN];
-      turn.load(n / (A.H * A.W), n / A.W % A.H, n % A.W, cs);
-#pragma unroll
-      for (int i = 0; i < CPT; ++i) turn.apply(g[i], cs, -1.f, scratch, lane);
-    }
-    if (norm != VEDA_NORM_NONE) {
-      float s1[CPT], s2[CPT];
-#pragma unroll
-      for (int i = 0; i < CPT; ++i) {
-        s1[i] = s2[i] = 0.f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          s1[i] = fmaf(v[i][k], v[i][k], s1[i]);
-          s2[i] = fmaf(g[i][k] * w[i][k], v[i][k], s2[i]);
+        for (int i = 0; i < CPT; ++i) {
+          const int head = head0 + i * head_step;
+          if (g.t + i * g.tpt < nchunk) {
+            rg.fetch(slot, i, dout + (row + (long long)head * A.N) * A.d);
+            if (norm != VEDA_NORM_NONE) rx.fetch(slot, i, in + at.b * sb + at.n * sn + head * sh);
+          }
         }
       }
-      if (norm == VEDA_NORM_ROW) {
-        float a = 0.f, c = 0.f;
+      cp_async_commit();
+    };
+#pragma unroll 1
+    for (int s = 0; s < D; ++s) fetch(first + s * step, s, s);
+    float w[CPT][8], acc[CPT][8];
 #pragma unroll
-        for (int i = 0; i < CPT; ++i) a += s1[i], c += s2[i];
-        if (W == 1) {
-          a = warp_sum(a);
-          c = warp_sum(c);
+    for (int i = 0; i < CPT; ++i) {
+      const int c = g.t + i * g.tpt;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc[i][k] = w[i][k] = 0.f;
+      if (norm != VEDA_NORM_NONE && c < nchunk) load8(A.w[which] + (norm == VEDA_NORM_ROW ? 8 * c : ch0), w[i]);
+    }
+    int slot = 0, aslot = 0;
+    auto next = [](int s, int n) { return s + 1 == n ? 0 : s + 1; };
+    for (int tok = first; tok < A.tokens; tok += step, flip ^= 1, slot = next(slot, D), aslot = next(aslot, D + 2)) {
+      const int b = A.by_n.div(tok), n = tok - b * A.N;
+      float gv[CPT][8], v[CPT][8];
+      cp_async_wait<D - 1>();
+#pragma unroll
+      for (int i = 0; i < CPT; ++i) {
+        rg.read(slot, i, gv[i]);
+        if (norm != VEDA_NORM_NONE) rx.read(slot, i, v[i]);
+        if (g.t + i * g.tpt >= nchunk) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) gv[i][k] = v[i][k] = 0.f;
+        }
+      }
+      fetch(tok + D * step, slot, aslot >= 2 ? aslot - 2 : aslot + D);
+      if (which < 2) {
+        group_sync(g);
+        float2 cs[Angles<HALVES, D>::kN];
+        angles.read(aslot, ch0, cs);
+#pragma unroll
+        for (int i = 0; i < CPT; ++i) angles.apply(gv[i], cs, -1.f, scratch, g.lane);
+      }
+      if (norm != VEDA_NORM_NONE) {
+        float s1[CPT], s2[CPT];
+#pragma unroll
+        for (int i = 0; i < CPT; ++i) {
+          s1[i] = s2[i] = 0.f;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            s1[i] = fmaf(v[i][k], v[i][k], s1[i]);
+            s2[i] = fmaf(gv[i][k] * w[i][k], v[i][k], s2[i]);
+          }
+        }
+        if (norm == VEDA_NORM_ROW) {
+          float a = 0.f, c = 0.f;
+#pragma unroll
+          for (int i = 0; i < CPT; ++i) a += s1[i], c += s2[i];
+          row_sum2(g, a, c, red, flip);
+#pragma unroll
+          for (int i = 0; i < CPT; ++i) s1[i] = a, s2[i] = c;
         } else {
-          // two sums per token: each has its own half of `red`, and the
-          // second's barrier stands between the first's next use and its readers
-          a = cta_sum(a, red, W, warp, lane, 0);
-          c = cta_sum(c, red, W, warp, lane, 1);
+#pragma unroll
+          for (int i = 0; i < CPT; ++i) s1[i] = head_sum(s1[i], lph), s2[i] = head_sum(s2[i], lph);
         }
 #pragma unroll
-        for (int i = 0; i < CPT; ++i) s1[i] = a, s2[i] = c;
-      } else {
+        for (int i = 0; i < CPT; ++i) {
+          const float rstd = rsqrtf(s1[i] * A.inv_n + A.eps), c1 = s2[i] * A.inv_n * rstd * rstd;
 #pragma unroll
-        for (int i = 0; i < CPT; ++i) s1[i] = head_sum(s1[i], lph), s2[i] = head_sum(s2[i], lph);
+          for (int k = 0; k < 8; ++k) {
+            acc[i][k] = fmaf(gv[i][k] * rstd, v[i][k], acc[i][k]);
+            gv[i][k] = rstd * (gv[i][k] * w[i][k] - v[i][k] * c1);
+          }
+        }
       }
 #pragma unroll
       for (int i = 0; i < CPT; ++i) {
-        const float rstd = rsqrtf(s1[i] * inv_n + A.eps), c1 = s2[i] * inv_n * rstd * rstd;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          acc[i][k] = fmaf(g[i][k] * rstd, v[i][k], acc[i][k]);
-          g[i][k] = rstd * (g[i][k] * w[i][k] - v[i][k] * c1);
-        }
+        const int head = head0 + i * head_step;
+        if (g.t + i * g.tpt < nchunk && VEDA_IN_BOUNDS(head < A.heads && tok < A.tokens))
+          store8(dx + b * dsb + n * dsn + head * dsh, gv[i]);
       }
     }
-#pragma unroll
-    for (int i = 0; i < CPT; ++i) {
-      const int c = t + i * tpt;
-      if (c < nchunk) store8(dx + b * dsb + n * dsn + (head0 + i * head_step) * dsh + ch0, g[i]);
-    }
-  }
-  float* part = A.part[which];
-  if (norm == VEDA_NORM_NONE || part == nullptr) return;   // CTA-uniform
-  if (norm == VEDA_NORM_ROW) {
-    const long long p = (long long)blockIdx.x * per_cta + (W == 1 ? warp : 0);
-#pragma unroll
-    for (int i = 0; i < CPT; ++i) {
-      const int c = t + i * tpt;
-      if (c < nchunk && VEDA_IN_BOUNDS(p < A.parts)) store8(part + p * (A.heads * A.d) + 8 * c, acc[i]);
-    }
-  } else {
-    // One weight row for all heads: add the thread's chunks, the lanes that
-    // share channels, then the warps in order.
-    float a[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      a[k] = 0.f;
-#pragma unroll
-      for (int i = 0; i < CPT; ++i) a[k] += acc[i][k];
-      for (int off = 16; off >= lph; off >>= 1) a[k] += __shfl_xor_sync(0xffffffffu, a[k], off);
-    }
-    float* all = scratch_all;   // d floats per warp (at most 128 of the warp's 288)
+    float* part = A.part[which];
+    if (norm == VEDA_NORM_NONE || part == nullptr) continue;   // CTA-uniform
+    // The CTA's weight gradient: one partial row per group (row norm) or per
+    // run of lanes with a head's channels (head norm), over the idle ring,
+    // added in order.
+    const int C = norm == VEDA_NORM_ROW ? A.heads * A.d : A.d;
+    const int n_rows = norm == VEDA_NORM_ROW ? g.groups : (int)blockDim.x / lph;
+    float* sums = reinterpret_cast<float*>(ring_raw);
+    cp_async_wait<0>();
     __syncthreads();
-    if (lane < lph) {
+    if (norm == VEDA_NORM_ROW) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) all[warp * 288 + lane * 8 + k] = a[k];
+      for (int i = 0; i < CPT; ++i) {
+        const int c = g.t + i * g.tpt;
+        if (c < nchunk) store8(sums + g.group * C + 8 * c, acc[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 1; i < CPT; ++i) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[0][k] += acc[i][k];
+      }
+      store8(sums + (threadIdx.x / lph) * C + ch0, acc[0]);
     }
     __syncthreads();
-    for (int c = threadIdx.x; c < A.d; c += blockDim.x) {
+    for (int c = threadIdx.x; c < C; c += blockDim.x) {
       float s = 0.f;
-      for (int k = 0; k < (int)(blockDim.x >> 5); ++k) s += all[k * 288 + c];
-      if (VEDA_IN_BOUNDS((int)blockIdx.x < A.parts)) part[(long long)blockIdx.x * A.d + c] = s;
+      for (int k = 0; k < n_rows; ++k) s += sums[k * C + c];
+      if (VEDA_IN_BOUNDS((int)blockIdx.x < A.parts)) part[(long long)blockIdx.x * C + c] = s;
     }
+    __syncthreads();
   }
 }
 
@@ -341,81 +436,64 @@ __global__ void rope_table_kernel(int n, int pairs, int dim, double log2_theta, 
 
 namespace {
 
-struct TokenSplit {
-  int cpt, warps, threads, per_cta;
-  size_t smem;
-};
-TokenSplit token_split(int nchunk, int max_cpt) {
-  TokenSplit r;
-  if (nchunk <= 32 * max_cpt) {
-    r.cpt = nchunk <= 32 ? 1 : nchunk <= 64 ? 2 : 4;
-    r.warps = 1;
-  } else {
-    r.cpt = nchunk <= 512 * 2 ? 2 : 4;
-    r.warps = (nchunk + 32 * r.cpt - 1) / (32 * r.cpt);
-  }
-  r.threads = r.warps == 1 ? 128 : 32 * r.warps;
-  r.per_cta = r.warps == 1 ? 4 : 1;
-  r.smem = (size_t)(r.threads / 32) * 32 * 9 * sizeof(float);
-  return r;
+unsigned rope_grid(int tokens, const RowSplit& r, unsigned most) {
+  const unsigned want = (unsigned)((tokens + r.groups - 1) / r.groups);
+  return want < most ? want : most;
 }
 
-unsigned rope_grid(long long tokens, const TokenSplit& r, int sms) {
-  const long long want = (tokens + r.per_cta - 1) / r.per_cta, most = (long long)sms * (2048 / r.threads);
-  return (unsigned)(want < most ? want : most);
-}
-
-template <typename T, bool HALVES>
-cudaError_t rope_run(const RopeArgs& a, const TokenSplit& r, dim3 grid, bool backward, cudaStream_t s) {
-  const size_t smem = HALVES || backward ? r.smem : 0;
-#define VEDA_ROPE(CPT)                                                                          \
-  if (r.cpt == CPT) {                                                                           \
-    if (backward) qkv_rope_bwd_kernel<T, CPT, HALVES><<<grid, r.threads, smem, s>>>(a);         \
-    else qkv_rope_kernel<T, CPT, HALVES><<<grid, r.threads, smem, s>>>(a);                      \
+template <typename T, int CPT, bool HALVES>
+cudaError_t rope_run(RopeArgs a, const RowSplit& r, bool backward, int sms, cudaStream_t s) {
+  const auto kernel = backward ? qkv_rope_bwd_kernel<T, CPT, HALVES> : qkv_rope_kernel<T, CPT, HALVES>;
+  const size_t ring = backward ? rope_bwd_depth(CPT) * (Ring<T, CPT>::kBytes + Ring<__nv_bfloat16, CPT>::kBytes)
+                               : rope_depth(CPT) * Ring<T, CPT>::kBytes;
+  const size_t angles = backward ? Angles<HALVES, rope_bwd_depth(CPT)>::kBytes : Angles<HALVES, rope_depth(CPT)>::kBytes;
+  const size_t smem = ring * r.threads + angles * r.groups + (HALVES ? r.threads * 9 * sizeof(float) : 0);
+  cudaError_t e = allow_smem(kernel, smem);
+  if (e != cudaSuccess) return e;
+  unsigned most = resident_ctas(kernel, r.threads, smem, sms);
+  if (backward && most > (unsigned)(kBwdCtasPerSm * sms)) most = kBwdCtasPerSm * sms;
+  const unsigned grid = rope_grid((int)a.tokens, r, most);
+  a.parts = (int)grid;
+  kernel<<<grid, r.threads, smem, s>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !backward) return e;
+  SumArgs sum;
+  sum.parts = a.parts;
+  sum.C = a.norm == VEDA_NORM_ROW ? a.heads * a.d : a.d;
+  int n = 0;
+  for (int i = 0; i < 2; ++i) {
+    if (a.part[i] == nullptr) continue;
+    sum.part[n] = a.part[i];
+    sum.out[n++] = a.dw[i];
   }
-  VEDA_ROPE(1) else VEDA_ROPE(2) else VEDA_ROPE(4)
-#undef VEDA_ROPE
-  return cudaGetLastError();
+  return n == 0 ? e : launch_sum_partials(sum, n, s);
 }
 
 template <typename T>
-cudaError_t rope_pairing(const RopeArgs& a, const TokenSplit& r, dim3 grid, bool backward, cudaStream_t s) {
-  return a.halves ? rope_run<T, true>(a, r, grid, backward, s) : rope_run<T, false>(a, r, grid, backward, s);
-}
-
-cudaError_t rope_types(const RopeArgs& a, int type, const TokenSplit& r, dim3 grid, bool backward, cudaStream_t s) {
-  if (type == VEDA_BF16) return rope_pairing<__nv_bfloat16>(a, r, grid, backward, s);
-  if (type == VEDA_FP16) return rope_pairing<__half>(a, r, grid, backward, s);
-  return rope_pairing<float>(a, r, grid, backward, s);
+cudaError_t rope_run(const RopeArgs& a, const RowSplit& r, bool backward, int sms, cudaStream_t s) {
+  if (r.cpt == 1) return a.halves ? rope_run<T, 1, true>(a, r, backward, sms, s) : rope_run<T, 1, false>(a, r, backward, sms, s);
+  if (r.cpt == 2) return a.halves ? rope_run<T, 2, true>(a, r, backward, sms, s) : rope_run<T, 2, false>(a, r, backward, sms, s);
+  return a.halves ? rope_run<T, 4, true>(a, r, backward, sms, s) : rope_run<T, 4, false>(a, r, backward, sms, s);
 }
 
 }  // namespace
 
-cudaError_t launch_qkv_rope(RopeArgs a, int type, int n_which, int sms, cudaStream_t s) {
-  const TokenSplit r = token_split(a.heads * a.d / 8, 4);
-  a.warps = r.warps;
-  return rope_types(a, type, r, dim3(rope_grid(a.tokens, r, sms), n_which), false, s);
+cudaError_t launch_qkv_rope(RopeArgs a, int type, bool backward, int sms, cudaStream_t s) {
+  const RowSplit r = row_split(a.heads * a.d / 8, a.tokens, sms);
+  a.warps = r.W;
+  a.HW = a.H * a.W;
+  a.by_n = FastDiv(a.N);
+  a.by_hw = FastDiv(a.HW);
+  a.by_w = FastDiv(a.W);
+  a.inv_n = 1.f / (float)(a.norm == VEDA_NORM_ROW ? a.heads * a.d : a.d);
+  if (type == VEDA_BF16) return rope_run<__nv_bfloat16>(a, r, backward, sms, s);
+  if (type == VEDA_FP16) return rope_run<__half>(a, r, backward, sms, s);
+  return rope_run<float>(a, r, backward, sms, s);
 }
 
-// Rows of weight-gradient partials, each heads*d (row norm) or d (head norm) floats.
-int qkv_rope_bwd_parts(long long tokens, int heads, int d, bool row, int sms) {
-  const TokenSplit r = token_split(heads * d / 8, 2);
-  return (int)rope_grid(tokens, r, sms) * (row ? r.per_cta : 1);
-}
-
-cudaError_t launch_qkv_rope_bwd(RopeArgs a, int type, int n_which, float* const* dw, int sms, cudaStream_t s) {
-  const TokenSplit r = token_split(a.heads * a.d / 8, 2);
-  a.warps = r.warps;
-  a.parts = qkv_rope_bwd_parts(a.tokens, a.heads, a.d, a.norm == VEDA_NORM_ROW, sms);
-  cudaError_t e = rope_types(a, type, r, dim3(rope_grid(a.tokens, r, sms), n_which), true, s);
-  if (e != cudaSuccess || a.norm == VEDA_NORM_NONE) return e;
-  const int C = a.norm == VEDA_NORM_ROW ? a.heads * a.d : a.d;
-  for (int i = 0; i < n_which; ++i) {
-    const int which = a.order[i];
-    if (which == 2 || dw[which] == nullptr) continue;
-    if ((e = launch_sum_partials(a.part[which], a.parts, C, dw[which], s)) != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+// Rows of weight-gradient partials at most, each heads*d (row norm) or d (head norm) floats.
+int qkv_rope_bwd_parts(long long tokens, int heads, int d, int sms) {
+  return (int)rope_grid((int)tokens, row_split(heads * d / 8, tokens, sms), kBwdCtasPerSm * sms);
 }
 
 cudaError_t launch_rope_table(int n, int dim, double theta, double start, double step, float* out, cudaStream_t s) {

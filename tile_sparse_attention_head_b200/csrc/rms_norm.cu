@@ -12,14 +12,14 @@
 // Sums and the statistics are fp32; h, y, dx and d_delta are rounded once.
 //
 // Every operand is read once and written once, so HBM is the bound.  A row is
-// held in registers between the sum and the output.  Rows of up to 1,024
-// channels take one warp each (four rows per CTA, no barrier), longer ones a
-// CTA of as many warps as the row needs; CTAs stay and step over the rows,
-// with the weights kept in registers.
+// held in registers between the sum and the output, by a group of as many warps
+// as it needs (one for up to 512 channels); groups stay and step over the rows.
+// The rows to come are on their way to shared memory meanwhile, so loads stay
+// in flight through the reduction's barrier and the stores.
 //
-// dw: each CTA (each warp for short rows) sums its own rows in registers and
-// writes one partial row; a second kernel adds the partial rows in a fixed
-// order.  No atomics, so a rerun gives the same bits.
+// dw: each group sums its own rows in registers, a CTA adds its groups in shared
+// memory and writes one partial row, and a second kernel adds the partial rows,
+// all in a fixed order.  No atomics, so a rerun gives the same bits.
 #include "layer_common.cuh"
 #include "kernels.h"
 #undef VEDA_SRC_ID
@@ -27,61 +27,74 @@
 
 namespace veda {
 
+// Rows in flight per group: what fits two CTAs of 16-bit rows on an SM.
+__host__ __device__ constexpr int norm_depth(int cpt) { return cpt == 4 ? 1 : 3; }
+__host__ __device__ constexpr int norm_bwd_depth(int cpt) { return cpt == 4 ? 1 : 2; }
+
 template <typename TX, typename TD, int CPT, bool FP8>
 __global__ void __launch_bounds__(512) add_rms_norm_kernel(const __grid_constant__ NormArgs A) {
-  __shared__ float red[64];
-  const int W = A.warps;                        // warps per row
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per_cta = W == 1 ? (int)(blockDim.x >> 5) : 1;
-  const int t = W == 1 ? lane : threadIdx.x;
-  const int tpt = 32 * W, nchunk = A.C / 8;
-  const TX* x = static_cast<const TX*>(A.x);
-  const TD* delta = static_cast<const TD*>(A.delta);
+  constexpr int D = norm_depth(CPT);
+  __shared__ float red[kRowRed];
+  extern __shared__ uint4 ring_raw[];
+  const RowGroup g(A.warps);
+  const Ring<TX, CPT> rx(ring_raw);
+  const Ring<TD, CPT> rd(ring_raw + D * Ring<TX, CPT>::kBytes / 16 * blockDim.x);
+  const int nchunk = A.C / 8;
+  const TX* x = static_cast<const TX*>(A.x) + 8 * g.t;
+  const TD* delta = A.delta == nullptr ? nullptr : static_cast<const TD*>(A.delta) + 8 * g.t;
   TX* h = static_cast<TX*>(A.h);
   float w[CPT][8];
 #pragma unroll
   for (int i = 0; i < CPT; ++i) {
-    const int c = t + i * tpt;
+    const int c = g.t + i * g.tpt;
     if (c < nchunk) load8(A.w + 8 * c, w[i]);
   }
   const float inv_c = 1.f / (float)A.C;
-  int turn = 0;
-  for (long long row = (long long)blockIdx.x * per_cta + (W == 1 ? warp : 0); row < A.rows;
-       row += (long long)gridDim.x * per_cta, turn ^= 1) {
-    float v[CPT][8];
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < CPT; ++i) {
-      const int c = t + i * tpt;
-      if (c < nchunk && VEDA_IN_BOUNDS(row < A.rows)) load8(x + row * A.ldx + 8 * c, v[i]);
-    }
-    if (delta != nullptr) {
+  const long long step = (long long)gridDim.x * g.groups;
+  auto fetch = [&](long long row, int slot) {
+    if (row < A.rows) {
 #pragma unroll
       for (int i = 0; i < CPT; ++i) {
-        const int c = t + i * tpt;
-        if (c < nchunk) {
-          float d[8];
-          load8(delta + row * A.ldd + 8 * c, d);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[i][k] = round_to<TX>(v[i][k] + d[k]);
+        if (g.t + i * g.tpt < nchunk) {
+          rx.fetch(slot, i, x + row * A.ldx + 8 * i * g.tpt);
+          if (delta != nullptr) rd.fetch(slot, i, delta + row * A.ldd + 8 * i * g.tpt);
         }
       }
     }
+    cp_async_commit();
+  };
+  long long row = (long long)blockIdx.x * g.groups + g.group;
+#pragma unroll 1
+  for (int s = 0; s < D; ++s) fetch(row + s * step, s);
+  for (int turn = 0, slot = 0; row < A.rows; row += step, turn ^= 1, slot = slot + 1 == D ? 0 : slot + 1) {
+    float v[CPT][8];
+    cp_async_wait<D - 1>();
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
-      const int c = t + i * tpt;
+      rx.read(slot, i, v[i]);
+      if (delta != nullptr) {
+        float d[8];
+        rd.read(slot, i, d);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[i][k] = round_to<TX>(v[i][k] + d[k]);
+      }
+    }
+    fetch(row + D * step, slot);
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+      const int c = g.t + i * g.tpt;
       if (c < nchunk) {
-        if (h != nullptr) store8(h + row * A.C + 8 * c, v[i]);
+        if (h != nullptr && VEDA_IN_BOUNDS(row < A.rows)) store8(h + row * A.C + 8 * c, v[i]);
 #pragma unroll
         for (int k = 0; k < 8; ++k) ss = fmaf(v[i][k], v[i][k], ss);
       }
     }
-    ss = W == 1 ? warp_sum(ss) : cta_sum(ss, red, W, warp, lane, turn);
-    const float rstd = rsqrtf(ss * inv_c + A.eps);
-    if (A.rstd != nullptr && t == 0) A.rstd[row] = rstd;
+    const float rstd = rsqrtf(row_sum(g, ss, red, turn) * inv_c + A.eps);
+    if (A.rstd != nullptr && g.t == 0) A.rstd[row] = rstd;
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
-      const int c = t + i * tpt;
+      const int c = g.t + i * g.tpt;
       float y[8];
       if (c < nchunk) {
 #pragma unroll
@@ -110,182 +123,208 @@ __global__ void __launch_bounds__(512) add_rms_norm_kernel(const __grid_constant
 
 template <typename TX, typename TD, int CPT>
 __global__ void __launch_bounds__(512) add_rms_norm_bwd_kernel(const __grid_constant__ NormBwdArgs A) {
-  __shared__ float red[64];
-  const int W = A.warps;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per_cta = W == 1 ? (int)(blockDim.x >> 5) : 1;
-  const int t = W == 1 ? lane : threadIdx.x;
-  const int tpt = 32 * W, nchunk = A.C / 8;
-  const TX* h = static_cast<const TX*>(A.h);
-  const TX* dh = static_cast<const TX*>(A.dh);
-  const TD* dy = static_cast<const TD*>(A.dy);
+  constexpr int D = norm_bwd_depth(CPT);
+  __shared__ float red[kRowRed];
+  extern __shared__ uint4 ring_raw[];
+  const RowGroup g(A.warps);
+  const Ring<TX, CPT> rh(ring_raw), rdh(ring_raw + D * Ring<TX, CPT>::kBytes / 16 * blockDim.x);
+  const Ring<TD, CPT> rdy(ring_raw + 2 * D * Ring<TX, CPT>::kBytes / 16 * blockDim.x);
+  const int nchunk = A.C / 8;
+  const TX* h = static_cast<const TX*>(A.h) + 8 * g.t;
+  const TX* dh = A.dh == nullptr ? nullptr : static_cast<const TX*>(A.dh) + 8 * g.t;
+  const TD* dy = static_cast<const TD*>(A.dy) + 8 * g.t;
   float w[CPT][8], acc[CPT][8];
 #pragma unroll
   for (int i = 0; i < CPT; ++i) {
-    const int c = t + i * tpt;
+    const int c = g.t + i * g.tpt;
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc[i][k] = 0.f;
     if (c < nchunk) load8(A.w + 8 * c, w[i]);
   }
   const float inv_c = 1.f / (float)A.C;
-  int turn = 0;
-  const long long first = (long long)blockIdx.x * per_cta + (W == 1 ? warp : 0);
-  for (long long row = first; row < A.rows; row += (long long)gridDim.x * per_cta, turn ^= 1) {
-    float hv[CPT][8], g[CPT][8];
-    float s = 0.f;
-    const float rstd = A.rstd[row];
+  const long long step = (long long)gridDim.x * g.groups;
+  auto fetch = [&](long long row, int slot) {
+    if (row < A.rows) {
 #pragma unroll
-    for (int i = 0; i < CPT; ++i) {
-      const int c = t + i * tpt;
-      if (c < nchunk && VEDA_IN_BOUNDS(row < A.rows)) {
-        load8(h + row * A.C + 8 * c, hv[i]);
-        load8(dy + row * A.C + 8 * c, g[i]);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < CPT; ++i) {
-      const int c = t + i * tpt;
-      if (c < nchunk) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          acc[i][k] = fmaf(g[i][k] * rstd, hv[i][k], acc[i][k]);
-          g[i][k] *= w[i][k];
-          s = fmaf(g[i][k], hv[i][k], s);
+      for (int i = 0; i < CPT; ++i) {
+        const long long at = row * A.C + 8 * i * g.tpt;
+        if (g.t + i * g.tpt < nchunk) {
+          rh.fetch(slot, i, h + at);
+          rdy.fetch(slot, i, dy + at);
+          if (dh != nullptr) rdh.fetch(slot, i, dh + at);
         }
       }
     }
-    s = W == 1 ? warp_sum(s) : cta_sum(s, red, W, warp, lane, turn);
+    cp_async_commit();
+  };
+  long long row = (long long)blockIdx.x * g.groups + g.group;
+#pragma unroll 1
+  for (int s = 0; s < D; ++s) fetch(row + s * step, s);
+  float nrstd = row < A.rows ? A.rstd[row] : 0.f;
+  for (int turn = 0, slot = 0; row < A.rows; row += step, turn ^= 1, slot = slot + 1 == D ? 0 : slot + 1) {
+    float hv[CPT][8], gv[CPT][8], dv[CPT][8];
+    float s = 0.f;
+    const float rstd = nrstd;
+    cp_async_wait<D - 1>();
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+      rh.read(slot, i, hv[i]);
+      rdy.read(slot, i, gv[i]);
+      if (dh != nullptr) {
+        rdh.read(slot, i, dv[i]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) dv[i][k] = 0.f;
+      }
+    }
+    fetch(row + D * step, slot);
+    if (row + step < A.rows) nrstd = A.rstd[row + step];
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+      if (g.t + i * g.tpt < nchunk) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          acc[i][k] = fmaf(gv[i][k] * rstd, hv[i][k], acc[i][k]);
+          gv[i][k] *= w[i][k];
+          s = fmaf(gv[i][k], hv[i][k], s);
+        }
+      }
+    }
+    s = row_sum(g, s, red, turn);
     const float c1 = s * inv_c * rstd * rstd;
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
-      const int c = t + i * tpt;
+      const int c = g.t + i * g.tpt;
       if (c < nchunk) {
-        float d[8];
-        if (dh != nullptr) {
-          load8(dh + row * A.C + 8 * c, d);
-        } else {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) d[k] = 0.f;
+        for (int k = 0; k < 8; ++k) dv[i][k] = fmaf(rstd, gv[i][k] - hv[i][k] * c1, dv[i][k]);
+        if (VEDA_IN_BOUNDS(row < A.rows)) {
+          if (A.dx != nullptr) store8(static_cast<TX*>(A.dx) + row * A.C + 8 * c, dv[i]);
+          if (A.ddelta != nullptr) store8(static_cast<TD*>(A.ddelta) + row * A.C + 8 * c, dv[i]);
         }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) d[k] = fmaf(rstd, g[i][k] - hv[i][k] * c1, d[k]);
-        if (A.dx != nullptr) store8(static_cast<TX*>(A.dx) + row * A.C + 8 * c, d);
-        if (A.ddelta != nullptr) store8(static_cast<TD*>(A.ddelta) + row * A.C + 8 * c, d);
       }
     }
   }
-  if (A.part != nullptr) {
-    const long long p = (long long)blockIdx.x * per_cta + (W == 1 ? warp : 0);
+  if (A.part == nullptr) return;
+  cp_async_wait<0>();
+  __syncthreads();
+  float* sums = reinterpret_cast<float*>(ring_raw);   // [groups, C], over the ring
 #pragma unroll
-    for (int i = 0; i < CPT; ++i) {
-      const int c = t + i * tpt;
-      if (c < nchunk && VEDA_IN_BOUNDS(p < A.parts)) store8(A.part + p * A.C + 8 * c, acc[i]);
-    }
+  for (int i = 0; i < CPT; ++i) {
+    const int c = g.t + i * g.tpt;
+    if (c < nchunk) store8(sums + g.group * A.C + 8 * c, acc[i]);
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < A.C; c += blockDim.x) {
+    float s = 0.f;
+    for (int k = 0; k < g.groups; ++k) s += sums[k * A.C + c];
+    if (VEDA_IN_BOUNDS((int)blockIdx.x < A.parts)) A.part[(long long)blockIdx.x * A.C + c] = s;
   }
 }
 
 // out[c] = sum_p part[p, c] in a fixed order: warp w of a CTA adds rows w,
 // w + 32, ... of its 32 columns, then the 32 sums are added in order.
-__global__ void __launch_bounds__(1024) sum_partials_kernel(const float* __restrict__ part, int parts, int C,
-                                                            float* __restrict__ out) {
+// blockIdx.y: one of several such sums.
+__global__ void __launch_bounds__(1024) sum_partials_kernel(const __grid_constant__ SumArgs A) {
   __shared__ float s[32][33];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = blockIdx.x * 32 + lane;
+  const float* part = A.part[blockIdx.y];
   float a = 0.f;
-  if (c < C) {
+  if (c < A.C) {
 #pragma unroll 4
-    for (int p = warp; p < parts; p += 32) a += part[(long long)p * C + c];
+    for (int p = warp; p < A.parts; p += 32) a += part[(long long)p * A.C + c];
   }
   s[warp][lane] = a;
   __syncthreads();
-  if (warp == 0 && c < C) {
+  if (warp == 0 && c < A.C) {
     float r = 0.f;
 #pragma unroll
     for (int k = 0; k < 32; ++k) r += s[k][lane];
-    out[c] = r;
+    A.out[blockIdx.y][c] = r;
   }
 }
 
-cudaError_t launch_sum_partials(const float* part, int parts, int C, float* out, cudaStream_t s) {
-  sum_partials_kernel<<<(C + 31) / 32, 1024, 0, s>>>(part, parts, C, out);
+cudaError_t launch_sum_partials(const SumArgs& a, int n, cudaStream_t s) {
+  sum_partials_kernel<<<dim3((a.C + 31) / 32, n), 1024, 0, s>>>(a);
   return cudaGetLastError();
 }
 
 namespace {
 
-// Chunks per thread and warps per row for rows of nchunk chunks.
-struct RowSplit {
-  int cpt, warps, threads, per_cta;
-};
-RowSplit row_split(int nchunk, int max_cpt) {
-  RowSplit r;
-  if (nchunk <= 32 * max_cpt) {
-    r.cpt = nchunk <= 32 ? 1 : nchunk <= 64 ? 2 : 4;
-    r.warps = 1;
-  } else {
-    r.cpt = nchunk <= 512 * 2 ? 2 : 4;
-    r.warps = (nchunk + 32 * r.cpt - 1) / (32 * r.cpt);
-  }
-  r.threads = r.warps == 1 ? 128 : 32 * r.warps;
-  r.per_cta = r.warps == 1 ? 4 : 1;
-  return r;
+unsigned norm_grid(long long rows, const RowSplit& r, unsigned most) {
+  const long long want = (rows + r.groups - 1) / r.groups;
+  return (unsigned)(want < (long long)most ? want : most);
 }
 
-template <typename TX, typename TD>
-cudaError_t norm_fwd(const NormArgs& a, bool fp8, const RowSplit& r, unsigned grid, cudaStream_t s) {
-#define VEDA_NORM(CPT)                                                                    \
-  if (r.cpt == CPT) {                                                                     \
-    if (fp8) add_rms_norm_kernel<TX, TD, CPT, true><<<grid, r.threads, 0, s>>>(a);        \
-    else add_rms_norm_kernel<TX, TD, CPT, false><<<grid, r.threads, 0, s>>>(a);           \
-  }
-  VEDA_NORM(1) else VEDA_NORM(2) else VEDA_NORM(4)
-#undef VEDA_NORM
+template <typename TX, typename TD, int CPT, bool FP8>
+cudaError_t norm_fwd(const NormArgs& a, const RowSplit& r, int sms, cudaStream_t s) {
+  const auto kernel = add_rms_norm_kernel<TX, TD, CPT, FP8>;
+  const size_t smem = (size_t)norm_depth(CPT) * (Ring<TX, CPT>::kBytes + Ring<TD, CPT>::kBytes) * r.threads;
+  const cudaError_t e = allow_smem(kernel, smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<norm_grid(a.rows, r, resident_ctas(kernel, r.threads, smem, sms)), r.threads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
 template <typename TX, typename TD>
-cudaError_t norm_bwd(const NormBwdArgs& a, const RowSplit& r, unsigned grid, cudaStream_t s) {
-  if (r.cpt == 1) add_rms_norm_bwd_kernel<TX, TD, 1><<<grid, r.threads, 0, s>>>(a);
-  else if (r.cpt == 2) add_rms_norm_bwd_kernel<TX, TD, 2><<<grid, r.threads, 0, s>>>(a);
-  else add_rms_norm_bwd_kernel<TX, TD, 4><<<grid, r.threads, 0, s>>>(a);
-  return cudaGetLastError();
+cudaError_t norm_fwd(const NormArgs& a, bool fp8, const RowSplit& r, int sms, cudaStream_t s) {
+  if (r.cpt == 1) return fp8 ? norm_fwd<TX, TD, 1, true>(a, r, sms, s) : norm_fwd<TX, TD, 1, false>(a, r, sms, s);
+  if (r.cpt == 2) return fp8 ? norm_fwd<TX, TD, 2, true>(a, r, sms, s) : norm_fwd<TX, TD, 2, false>(a, r, sms, s);
+  return fp8 ? norm_fwd<TX, TD, 4, true>(a, r, sms, s) : norm_fwd<TX, TD, 4, false>(a, r, sms, s);
 }
 
-unsigned norm_grid(long long rows, const RowSplit& r, int sms) {
-  const long long want = (rows + r.per_cta - 1) / r.per_cta, most = (long long)sms * (2048 / r.threads);
-  return (unsigned)(want < most ? want : most);
+template <typename TX, typename TD, int CPT>
+cudaError_t norm_bwd(NormBwdArgs a, const RowSplit& r, int sms, cudaStream_t s) {
+  const auto kernel = add_rms_norm_bwd_kernel<TX, TD, CPT>;
+  const size_t smem = (size_t)norm_bwd_depth(CPT) * (2 * Ring<TX, CPT>::kBytes + Ring<TD, CPT>::kBytes) * r.threads;
+  cudaError_t e = allow_smem(kernel, smem);
+  if (e != cudaSuccess) return e;
+  unsigned most = resident_ctas(kernel, r.threads, smem, sms);
+  if (most > (unsigned)(kBwdCtasPerSm * sms)) most = kBwdCtasPerSm * sms;
+  const unsigned grid = norm_grid(a.rows, r, most);
+  a.parts = (int)grid;
+  kernel<<<grid, r.threads, smem, s>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || a.part == nullptr) return e;
+  SumArgs sum;
+  sum.part[0] = a.part;
+  sum.out[0] = a.dw;
+  sum.parts = a.parts;
+  sum.C = a.C;
+  return launch_sum_partials(sum, 1, s);
+}
+
+template <typename TX, typename TD>
+cudaError_t norm_bwd(const NormBwdArgs& a, const RowSplit& r, int sms, cudaStream_t s) {
+  if (r.cpt == 1) return norm_bwd<TX, TD, 1>(a, r, sms, s);
+  if (r.cpt == 2) return norm_bwd<TX, TD, 2>(a, r, sms, s);
+  return norm_bwd<TX, TD, 4>(a, r, sms, s);
 }
 
 }  // namespace
 
 cudaError_t launch_add_rms_norm(NormArgs a, int tx, int td, bool fp8, int sms, cudaStream_t s) {
-  const RowSplit r = row_split(a.C / 8, 4);
-  a.warps = r.warps;
-  const unsigned grid = norm_grid(a.rows, r, sms);
-  if (tx == VEDA_BF16) return norm_fwd<__nv_bfloat16, __nv_bfloat16>(a, fp8, r, grid, s);
-  if (tx == VEDA_FP16) return norm_fwd<__half, __half>(a, fp8, r, grid, s);
-  if (td == VEDA_FP32) return norm_fwd<float, float>(a, fp8, r, grid, s);
-  return norm_fwd<float, __nv_bfloat16>(a, fp8, r, grid, s);
+  const RowSplit r = row_split(a.C / 8, a.rows, sms);
+  a.warps = r.W;
+  if (tx == VEDA_BF16) return norm_fwd<__nv_bfloat16, __nv_bfloat16>(a, fp8, r, sms, s);
+  if (tx == VEDA_FP16) return norm_fwd<__half, __half>(a, fp8, r, sms, s);
+  if (td == VEDA_FP32) return norm_fwd<float, float>(a, fp8, r, sms, s);
+  return norm_fwd<float, __nv_bfloat16>(a, fp8, r, sms, s);
 }
 
-// Partial rows of dw: one per CTA, or per warp where a warp has a row.
+// Partial rows of dw at most: one per CTA.
 int add_rms_norm_bwd_parts(long long rows, int C, int sms) {
-  const RowSplit r = row_split(C / 8, 2);
-  return (int)norm_grid(rows, r, sms) * r.per_cta;
+  return (int)norm_grid(rows, row_split(C / 8, rows, sms), kBwdCtasPerSm * sms);
 }
 
-cudaError_t launch_add_rms_norm_bwd(NormBwdArgs a, int tx, int td, float* dw, int sms, cudaStream_t s) {
-  const RowSplit r = row_split(a.C / 8, 2);
-  a.warps = r.warps;
-  a.parts = add_rms_norm_bwd_parts(a.rows, a.C, sms);
-  const unsigned grid = norm_grid(a.rows, r, sms);
-  cudaError_t e;
-  if (tx == VEDA_BF16) e = norm_bwd<__nv_bfloat16, __nv_bfloat16>(a, r, grid, s);
-  else if (tx == VEDA_FP16) e = norm_bwd<__half, __half>(a, r, grid, s);
-  else if (td == VEDA_FP32) e = norm_bwd<float, float>(a, r, grid, s);
-  else e = norm_bwd<float, __nv_bfloat16>(a, r, grid, s);
-  if (e != cudaSuccess || dw == nullptr) return e;
-  return launch_sum_partials(a.part, a.parts, a.C, dw, s);
+cudaError_t launch_add_rms_norm_bwd(NormBwdArgs a, int tx, int td, int sms, cudaStream_t s) {
+  const RowSplit r = row_split(a.C / 8, a.rows, sms);
+  a.warps = r.W;
+  if (tx == VEDA_BF16) return norm_bwd<__nv_bfloat16, __nv_bfloat16>(a, r, sms, s);
+  if (tx == VEDA_FP16) return norm_bwd<__half, __half>(a, r, sms, s);
+  if (td == VEDA_FP32) return norm_bwd<float, float>(a, r, sms, s);
+  return norm_bwd<float, __nv_bfloat16>(a, r, sms, s);
 }
 
 }  // namespace veda

@@ -22,29 +22,42 @@ from torch.autograd.function import once_differentiable
 from . import binding as B
 
 
+def _wants_grad(*tensors) -> bool:
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                return True
+    return False
+
+
 def _no_grad_inputs(func: str, *tensors) -> None:
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+    if _wants_grad(*tensors):
         raise ValueError(f"{func} is an inference operator: it has no gradient (call it under torch.no_grad())")
 
 
-def _wants_grad(*tensors) -> bool:
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
-
-
 def _flat(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
-    """[..., C] as rows [R, C] with contiguous channels (a copy only if the strides need one)."""
+    """[..., C] as rows [R, C] that the library can read in place: contiguous channels, 16-byte aligned rows that do
+    not overlap; a copy only where the tensor is not like that (a broadcast one, say)."""
     if t is None:
         return None
     if t.dim() != 2:
-        t = t.reshape(t.numel() // t.shape[-1] if t.shape[-1] else 0, t.shape[-1])
-    return t if t.shape[1] <= 1 or t.stride(1) == 1 else t.contiguous()
+        t = t.reshape(t.numel() // t.shape[-1] if t.dim() and t.shape[-1] else 0, t.shape[-1] if t.dim() else 0)
+    if t.is_contiguous():
+        return t
+    rows, C = t.shape
+    stride, step = t.stride()
+    return t if (step == 1 or C == 1) and (rows == 1 or (stride >= C and stride % 8 == 0)) else t.contiguous()
 
 
 def _dense(t: Optional[torch.Tensor], shape, dtype: Optional[torch.dtype] = None) -> Optional[torch.Tensor]:
     """An upstream gradient as the library reads it: dense, 16-byte aligned, of `shape`."""
     if t is None:
         return None
-    t = t.to(dtype or t.dtype).reshape(shape).contiguous()
+    if dtype is not None and t.dtype is not dtype:
+        t = t.to(dtype)
+    if t.shape != shape:
+        t = t.reshape(shape)
+    t = t.contiguous()
     return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
@@ -56,9 +69,12 @@ def _check_stream_and_delta(x: torch.Tensor, delta: Optional[torch.Tensor]) -> N
 # ---------------------------------------------------------------- residual and norm
 
 def _norm_forward(x, delta, weight, eps, want_rstd):
-    h = torch.empty(x.shape, dtype=x.dtype, device=x.device) if delta is not None else None
-    y = torch.empty(x.shape, dtype=x.dtype if delta is None else delta.dtype, device=x.device)
-    rstd = torch.empty(x.shape[0], dtype=torch.float32, device=x.device) if want_rstd else None
+    """Of rows x and delta; outputs are allocated like them (dense: an empty_like of rows with gaps has none)."""
+    if delta is None:
+        h, y = None, torch.empty_like(x)
+    else:
+        h, y = torch.empty_like(x), torch.empty_like(delta)
+    rstd = x.new_empty(x.shape[0], dtype=torch.float32) if want_rstd else None
     B.veda_add_rms_norm(x, delta, weight, eps, h, y, rstd)
     return h, y, rstd
 
@@ -70,37 +86,35 @@ class _AddRmsNorm(torch.autograd.Function):
     def forward(ctx, x, delta, weight, eps):
         x2, d2 = _flat(x), _flat(delta)
         h, y, rstd = _norm_forward(x2, d2, weight, eps, True)
-        if delta is None:
-            h = x2 if x2.is_contiguous() else x2.contiguous()
-        ctx.has_delta = delta is not None
-        ctx.delta_type = y.dtype
         ctx.set_materialize_grads(False)
+        ctx.like = None if delta is None else delta.dtype
+        if h is None:
+            ctx.save_for_backward(x2 if x2.is_contiguous() else x2.contiguous(), weight, rstd)
+            return y if x.dim() == 2 else y.view(x.shape)
         ctx.save_for_backward(h, weight, rstd)
-        y = y.view(x.shape)
-        return (h.view(x.shape), y) if ctx.has_delta else y
+        return (h, y) if x.dim() == 2 else (h.view(x.shape), y.view(x.shape))
 
     @staticmethod
     @once_differentiable
     def backward(ctx, *grads):
         h, weight, rstd = ctx.saved_tensors
-        dh, dy = grads if ctx.has_delta else (None, grads[0])
+        dh, dy = grads if len(grads) == 2 else (None, grads[0])
         want_x, want_d, want_w, _ = ctx.needs_input_grad
-        shape = h.shape if dy is None and dh is None else (dh if dy is None else dy).shape
         if dy is None:   # only the sum itself was used: its gradient goes to both addends
-            return dh if want_x else None, None if dh is None or not want_d else dh.to(ctx.delta_type), None, None
+            return dh if want_x else None, None if dh is None or not want_d else dh.to(ctx.like), None, None
+        shape = dy.shape
         dy, dh = _dense(dy, h.shape), _dense(dh, h.shape)
-        same = dy.dtype == h.dtype
+        same = dy.dtype is h.dtype
         dx = torch.empty_like(h) if want_x or (want_d and same) else None
         dd = torch.empty_like(dy) if want_d and not same else None
         dw = ws = None
         if want_w:
             dw = torch.empty_like(weight)
-            ws = torch.empty(B.veda_add_rms_norm_backward_workspace(*h.shape, h.device), dtype=torch.uint8,
-                             device=h.device)
+            ws = h.new_empty(B.veda_add_rms_norm_backward_workspace(*h.shape, h.get_device()), dtype=torch.uint8)
         B.veda_add_rms_norm_backward(h, dy, dh, weight, rstd, dx, dd, dw, ws)
-        gx = None if dx is None else dx.view(shape)
-        gd = gx if same else None if dd is None else dd.view(shape)
-        return gx if want_x else None, gd if want_d else None, dw, None
+        if len(shape) != 2:
+            dx, dd = None if dx is None else dx.view(shape), None if dd is None else dd.view(shape)
+        return dx if want_x else None, (dx if same else dd) if want_d else None, dw, None
 
 
 def add_rms_norm(x: torch.Tensor, delta: Optional[torch.Tensor], weight: torch.Tensor,
@@ -113,7 +127,9 @@ def add_rms_norm(x: torch.Tensor, delta: Optional[torch.Tensor], weight: torch.T
     _check_stream_and_delta(x, delta)
     if not _wants_grad(x, delta, weight):
         h, y, _ = _norm_forward(_flat(x), _flat(delta), weight, eps, False)
-        return (x if h is None else h.view(x.shape)), y.view(x.shape)
+        if x.dim() != 2:
+            h, y = None if h is None else h.view(x.shape), y.view(x.shape)
+        return (x if h is None else h), y
     if delta is None:
         return x, _AddRmsNorm.apply(x, None, weight, eps)
     return _AddRmsNorm.apply(x, delta, weight, eps)
@@ -126,11 +142,11 @@ def add_rms_norm_fp8(x: torch.Tensor, delta: Optional[torch.Tensor], weight: tor
     _check_stream_and_delta(x, delta)
     x2, d2 = _flat(x), _flat(delta)
     rows, C = x2.shape
-    h = torch.empty((rows, C), dtype=x.dtype, device=x.device) if delta is not None else None
-    y8 = torch.empty((rows, C), dtype=B.FP8, device=x.device)
-    scale = torch.empty(((C + 127) // 128, rows), dtype=torch.float32, device=x.device)
+    h = torch.empty_like(x2) if delta is not None else None
+    y8 = x2.new_empty((rows, C), dtype=B.FP8)
+    scale = x2.new_empty(((C + 127) // 128, rows), dtype=torch.float32)
     B.veda_add_rms_norm_fp8(x2, d2, weight, eps, h, y8, scale)
-    return (x if h is None else h.view(x.shape)), y8, scale
+    return x if h is None else h if x.dim() == 2 else h.view(x.shape), y8, scale
 
 
 # ---------------------------------------------------------------- 8-bit product
@@ -151,8 +167,8 @@ def quant_fp8_heads(o: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
 
 def _quant(x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
     rows, C = x.shape if x.dim() == 2 else (x.shape[0] * x.shape[2], x.shape[1] * x.shape[3])
-    q = torch.empty((rows, C), dtype=B.FP8, device=x.device)
-    scale = torch.empty(((C + 127) // 128, rows), dtype=torch.float32, device=x.device)
+    q = x.new_empty((rows, C), dtype=B.FP8)
+    scale = x.new_empty(((C + 127) // 128, rows), dtype=torch.float32)
     B.veda_quant_fp8(x, q, scale)
     return q, scale
 
@@ -172,7 +188,7 @@ def gemm_fp8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: t
     """[M, N] = a [M, K] @ b [N, K]^T (+ bias fp32 [N]) of e4m3 operands with a scale for each block of 128."""
     _no_grad_inputs("gemm_fp8", a_scale, b_scale, bias)
     if out is None:
-        out = torch.empty((a.shape[0], b.shape[0]), dtype=out_dtype, device=a.device)
+        out = a.new_empty((a.shape[0], b.shape[0]), dtype=out_dtype)
     return B.veda_gemm_fp8(a, a_scale, b, b_scale, bias, out)
 
 
@@ -199,18 +215,18 @@ class _QkvNormRope(torch.autograd.Function):
     def forward(ctx, rope, tables, wq, wk, *xs):
         q, k, v = xs[0].unbind(2) if len(xs) == 1 else xs
         shape = (rope.B, rope.heads, q.shape[1], rope.d)
-        outs = tuple(torch.empty(shape, dtype=torch.bfloat16, device=q.device) for _ in range(3))
+        outs = tuple(q.new_empty(shape, dtype=torch.bfloat16) for _ in range(3))
         B.veda_qkv_norm_rope(rope, q, k, v, wq, wk, *outs)
-        ctx.rope, ctx.tables, ctx.packed = rope, tables, len(xs) == 1     # tables: kept alive for backward
+        ctx.rope, ctx.packed = rope, len(xs) == 1
         ctx.set_materialize_grads(False)
-        ctx.save_for_backward(wq, wk, *xs)
+        ctx.save_for_backward(wq, wk, *tables, *xs)     # rope points into the tables: they must stay as they are
         return outs
 
     @staticmethod
     @once_differentiable
     def backward(ctx, *douts):
         rope = ctx.rope
-        wq, wk, *xs = ctx.saved_tensors
+        wq, wk, _, _, _, *xs = ctx.saved_tensors
         want_wq, want_wk, *want_x = ctx.needs_input_grad[2:]
         if ctx.packed:
             x = xs[0]
@@ -230,8 +246,7 @@ class _QkvNormRope(torch.autograd.Function):
             dwk = torch.empty_like(wk) if want_wk and need[1] else None
             ws = None
             if dwq is not None or dwk is not None:
-                ws = torch.empty(B.veda_qkv_norm_rope_backward_workspace(rope, q.device), dtype=torch.uint8,
-                                 device=q.device)
+                ws = q.new_empty(B.veda_qkv_norm_rope_backward_workspace(rope, q.get_device()), dtype=torch.uint8)
             B.veda_qkv_norm_rope_backward(rope, q, k, wq, wk, *d, *(x if n else None for x, n in zip(dxs, need)),
                                           dwq, dwk, ws)
         else:
@@ -271,13 +286,13 @@ def qkv_norm_rope(qkv, grid: Sequence[int], tables: Sequence[Optional[torch.Tens
     if norm == "none" and (wq is not None or wk is not None):
         raise ValueError("norm 'none' takes no weights")
     for t in tables:
-        if t is not None and t.device != xs[0].device:
+        if t is not None and t.get_device() != xs[0].get_device():
             raise ValueError(f"a table is on {t.device}, qkv on {xs[0].device}")
     rope = B.make_rope(b, heads, d, grid, tables, pairing, norm, eps)
     if _wants_grad(wq, wk, *xs):
         return _QkvNormRope.apply(rope, tuple(tables), wq, wk, *xs)
     q, k, v = xs[0].unbind(2) if len(xs) == 1 else xs
-    outs = tuple(torch.empty((b, heads, n, d), dtype=torch.bfloat16, device=q.device) for _ in range(3))
+    outs = tuple(q.new_empty((b, heads, n, d), dtype=torch.bfloat16) for _ in range(3))
     B.veda_qkv_norm_rope(rope, q, k, v, wq, wk, *outs)
     return outs
 
