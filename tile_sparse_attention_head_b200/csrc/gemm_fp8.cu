@@ -209,16 +209,13 @@ __global__ void __launch_bounds__(384, 1)
         for (int j = 0; j < HN / 8; ++j) {
           const int col = col0 + 8 * j;
           if (col >= A.N) break;
-          float v[8];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) f2_split(acc[4 * j + k], v[2 * k], v[2 * k + 1]);
           if (A.bias != nullptr) {
-            float b[8];
-            load8(A.bias + col, b);
+            uint64_t b[4];
+            load_pairs(A.bias + col, b);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] += b[k];
+            for (int k = 0; k < 4; ++k) acc[4 * j + k] = f2_add(acc[4 * j + k], b[k]);
           }
-          if (VEDA_IN_BOUNDS(row < A.M && col + 8 <= A.N)) store8(out + col, v);
+          if (VEDA_IN_BOUNDS(row < A.M && col + 8 <= A.N)) store_pairs(out + col, acc + 4 * j);
         }
       }
     }

@@ -145,6 +145,17 @@ cudaError_t launch_attn_bwd_dkdv(const Geometry& G, const BwdMaps<kMaxGridMaps>&
 
 // ---- operators around the attention ----
 
+// n / d for 0 <= n < 2^31 by one multiplication.
+struct FastDiv {
+  uint32_t d, mul, shift;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t divisor) : d(divisor), shift(0) {
+    while ((1ull << shift) < d) ++shift;
+    mul = (uint32_t)((((1ull << shift) - d) << 32) / d + 1);
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
+};
+
 struct NormArgs {
   long long rows;
   int C;
@@ -180,17 +191,6 @@ struct SumArgs {
 };
 constexpr int kBwdCtasPerSm = 3;   // of the kernels that write partial rows
 
-// n / d for 0 <= n < 2^31 by one multiplication.
-struct FastDiv {
-  uint32_t d, mul, shift;
-  FastDiv() = default;
-  explicit FastDiv(uint32_t divisor) : d(divisor), shift(0) {
-    while ((1ull << shift) < d) ++shift;
-    mul = (uint32_t)((((1ull << shift) - d) << 32) / d + 1);
-  }
-  __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
-};
-
 struct RopeArgs {
   int heads, d, H, W, HW, N;
   long long tokens;             // B * N, below 2^31
@@ -213,7 +213,8 @@ struct RopeArgs {
 
 struct QuantArgs {
   const void* x;
-  long long rows, N;            // rows = batches * N
+  long long rows, N;            // rows = batches * N, below 2^31
+  FastDiv by_n;
   int C, d;
   long long sb, sn, sh;
   uint8_t* q;
@@ -238,7 +239,7 @@ cudaError_t launch_qkv_rope(RopeArgs a, int type, bool backward, int sms, cudaSt
 int qkv_rope_bwd_parts(long long tokens, int heads, int d, int sms);
 cudaError_t launch_rope_table(int n, int dim, double theta, double start, double step, float* out, cudaStream_t s);
 
-cudaError_t launch_quant_rows(const QuantArgs& a, int type, cudaStream_t s);
+cudaError_t launch_quant_rows(QuantArgs a, int type, cudaStream_t s);
 cudaError_t launch_quant_weight(const void* w, int type, int N, int K, uint8_t* q, float* scale, cudaStream_t s);
 
 void gemm_fp8_boxes(const GemmArgs& a, int* rows_a, int* rows_b);

@@ -205,7 +205,7 @@ veda_status veda_quant_fp8(int32_t B, int64_t N, int32_t heads, int32_t d, veda_
   if (stride_b < 0 || stride_n < 0 || stride_h < 0 || stride_b % 8 || stride_n % 8 || stride_h % 8)
     return fail(VEDA_ERR_INVALID_ARG, "strides must be multiples of 8 and not negative");
   if (B == 0 || N == 0) return ok();
-  if (N > (1LL << 31) / B) return fail(VEDA_ERR_INVALID_ARG, "B*N exceeds 2^31 rows");
+  if (N >= (1LL << 31) / B) return fail(VEDA_ERR_INVALID_ARG, "B*N must be below 2^31 rows");
   if (!x || !q || !scale) return fail(VEDA_ERR_INVALID_ARG, "NULL tensor argument");
   if (!aligned16(x) || !aligned16(q) || !aligned16(scale))
     return fail(VEDA_ERR_INVALID_ARG, "tensor arguments must be 16-byte aligned");

@@ -11,39 +11,123 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "veda_common.cuh"
 
 namespace veda {
 
+// A chunk as it lies in memory, and as four pairs of fp32 (the arithmetic runs
+// on pairs: one issue slot for two channels).
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float* v);
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float* v) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+struct Words {
+  uint4 u[sizeof(T) / 2];
+};
+__device__ __forceinline__ void to_pairs(const Words<float>& x, uint64_t* p) {
+  p[0] = f2(__uint_as_float(x.u[0].x), __uint_as_float(x.u[0].y));
+  p[1] = f2(__uint_as_float(x.u[0].z), __uint_as_float(x.u[0].w));
+  p[2] = f2(__uint_as_float(x.u[1].x), __uint_as_float(x.u[1].y));
+  p[3] = f2(__uint_as_float(x.u[1].z), __uint_as_float(x.u[1].w));
 }
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float* v) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&u);
+__device__ __forceinline__ uint64_t bf16_pair(uint32_t w) {
+  return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ uint64_t fp16_pair(uint32_t w) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return f2(f.x, f.y);
+}
+__device__ __forceinline__ void to_pairs(const Words<__nv_bfloat16>& x, uint64_t* p) {
+  p[0] = bf16_pair(x.u[0].x), p[1] = bf16_pair(x.u[0].y), p[2] = bf16_pair(x.u[0].z), p[3] = bf16_pair(x.u[0].w);
+}
+__device__ __forceinline__ void to_pairs(const Words<__half>& x, uint64_t* p) {
+  p[0] = fp16_pair(x.u[0].x), p[1] = fp16_pair(x.u[0].y), p[2] = fp16_pair(x.u[0].z), p[3] = fp16_pair(x.u[0].w);
+}
+
+// Pairs rounded to T, nearest even.
+template <typename T>
+__device__ __forceinline__ Words<T> to_words(const uint64_t* p) {
+  Words<T> r;
+  if constexpr (sizeof(T) == 4) {
+    float v[8];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float2 f = __bfloat1622float2(b[k]);
-    v[2 * k] = f.x;
-    v[2 * k + 1] = f.y;
+    for (int k = 0; k < 4; ++k) f2_split(p[k], v[2 * k], v[2 * k + 1]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      r.u[k] = make_uint4(__float_as_uint(v[4 * k]), __float_as_uint(v[4 * k + 1]), __float_as_uint(v[4 * k + 2]),
+                          __float_as_uint(v[4 * k + 3]));
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float a, b;
+      f2_split(p[k], a, b);
+      if constexpr (std::is_same<T, __half>::value) {
+        const __half2 h = __floats2half2_rn(a, b);
+        w[k] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        w[k] = pack_bf16x2(a, b);
+      }
+    }
+    r.u[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void load_pairs(const T* p, uint64_t* v) {
+  Words<T> w;
+#pragma unroll
+  for (int k = 0; k < (int)(sizeof(T) / 2); ++k) w.u[k] = reinterpret_cast<const uint4*>(p)[k];
+  to_pairs(w, v);
+}
+template <typename T>
+__device__ __forceinline__ void store_words(T* p, const Words<T>& w) {
+#pragma unroll
+  for (int k = 0; k < (int)(sizeof(T) / 2); ++k) reinterpret_cast<uint4*>(p)[k] = w.u[k];
+}
+template <typename T>
+__device__ __forceinline__ void store_pairs(T* p, const uint64_t* v) { store_words(p, to_words<T>(v)); }
+
+// x + d rounded to x's type.  Of two 16-bit values the sum is exact in fp32, or
+// so far from a rounding border that one rounding and two agree, so the 16-bit
+// addition (two channels an instruction) gives what an fp32 sum rounded to 16
+// bits gives.
+template <typename T>
+__device__ __forceinline__ uint32_t add_words(uint32_t a, uint32_t b) {
+  if constexpr (std::is_same<T, __half>::value) {
+    const __half2 r = __hadd2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  } else {
+    const __nv_bfloat162 r =
+        __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
   }
 }
-template <>
-__device__ __forceinline__ void load8<__half>(const __half* p, float* v) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const __half2* b = reinterpret_cast<const __half2*>(&u);
+template <typename TX, typename TD>
+__device__ __forceinline__ void add_to(Words<TX>& x, const Words<TD>& d) {
+  if constexpr (sizeof(TX) == 2) {
+    x.u[0] = make_uint4(add_words<TX>(x.u[0].x, d.u[0].x), add_words<TX>(x.u[0].y, d.u[0].y),
+                        add_words<TX>(x.u[0].z, d.u[0].z), add_words<TX>(x.u[0].w, d.u[0].w));
+  } else {
+    uint64_t a[4], b[4];
+    to_pairs(x, a);
+    to_pairs(d, b);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float2 f = __half22float2(b[k]);
-    v[2 * k] = f.x;
-    v[2 * k + 1] = f.y;
+    for (int k = 0; k < 4; ++k) a[k] = f2_add(a[k], b[k]);
+    x = to_words<TX>(a);
   }
+}
+
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t f2_all(float a) { return f2(a, a); }
+__device__ __forceinline__ float f2_sum(uint64_t a) {
+  float lo, hi;
+  f2_split(a, lo, hi);
+  return lo + hi;
 }
 
 // Chunks on their way from global memory, D rows ahead of their use, in shared
@@ -76,44 +160,13 @@ struct Ring {
 #pragma unroll
     for (int k = 0; k < kPieces; ++k) cp_async16(smem_u32(at(slot, i, k)), reinterpret_cast<const uint4*>(p) + k);
   }
-  __device__ __forceinline__ void read(int slot, int i, float* v) const {
-    uint4 u[kPieces];
+  __device__ __forceinline__ Words<T> read(int slot, int i) const {
+    Words<T> w;
 #pragma unroll
-    for (int k = 0; k < kPieces; ++k) u[k] = *at(slot, i, k);
-    load8(reinterpret_cast<const T*>(u), v);
+    for (int k = 0; k < kPieces; ++k) w.u[k] = *at(slot, i, k);
+    return w;
   }
 };
-
-template <typename T>
-__device__ __forceinline__ void store8(T* p, const float* v);
-template <>
-__device__ __forceinline__ void store8<float>(float* p, const float* v) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
-template <>
-__device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* p, const float* v) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                            pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-}
-template <>
-__device__ __forceinline__ void store8<__half>(__half* p, const float* v) {
-  uint4 u;
-  __half2* b = reinterpret_cast<__half2*>(&u);
-#pragma unroll
-  for (int k = 0; k < 4; ++k) b[k] = __floats2half2_rn(v[2 * k], v[2 * k + 1]);
-  *reinterpret_cast<uint4*>(p) = u;
-}
-
-// v rounded to T and back: the value a stored element stands for.
-template <typename T>
-__device__ __forceinline__ float round_to(float v);
-template <>
-__device__ __forceinline__ float round_to<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ float round_to<__nv_bfloat16>(float v) { return __bfloat162float(__float2bfloat16_rn(v)); }
-template <>
-__device__ __forceinline__ float round_to<__half>(float v) { return __half2float(__float2half_rn(v)); }
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -201,21 +254,37 @@ inline unsigned resident_ctas(K kernel, int threads, size_t smem, int sms) {
 // The 8-bit rule: a block's scale is s = a / 448 with a its largest magnitude,
 // but at least 2^-100 (so that a block of zeros has a scale and 448 / a stays
 // finite), and the block holds e4m3(x * (448 / a)), nearest even.  The maximum
-// runs on the magnitudes' bit patterns, which order like the magnitudes and
-// put infinity and then NaN on top: a block with either gets a scale that is
-// infinite or NaN, and stands for NaN as a whole, rather than passing on a
-// finite wrong value.
+// passes NaN on: a block with an infinity or NaN gets a scale that is infinite
+// or NaN, and stands for NaN as a whole, rather than for a finite wrong value.
 constexpr float kE4M3Max = 448.f;
-constexpr uint32_t kTinyBits = (127u - 100u) << 23;   // 2^-100
+constexpr float kTiny = 7.888609052210118e-31f;   // 2^-100
 
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+// The larger of m and the pairs' magnitudes.
+__device__ __forceinline__ float max_abs(float m, const uint64_t* p) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float a, b;
+    f2_split(p[k], a, b);
+    asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(fabsf(a)), "f"(fabsf(b)));
+  }
+  return m;
+}
 
-__device__ __forceinline__ uint2 pack_e4m3x8(const float* v, float r) {
+__device__ __forceinline__ uint2 to_e4m3(const uint64_t* p, float r) {
+  const uint64_t rr = f2_all(r);
   uint32_t w[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    w[k] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * k] * r, v[2 * k + 1] * r), __NV_SATFINITE, __NV_E4M3);
-  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+  for (int k = 0; k < 4; ++k) {
+    float2 v;
+    f2_split(f2_mul(p[k], rr), v.x, v.y);
+    w[k] = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+  }
+  return make_uint2(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410));
 }
 
 }  // namespace veda

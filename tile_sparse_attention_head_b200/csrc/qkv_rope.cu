@@ -54,19 +54,6 @@ __device__ __forceinline__ PairOf pair_of(const RopeArgs& A, int ch) {
   return g;
 }
 
-// Place of a token: batch, index in the grid, and the grid's coordinates.
-struct Place {
-  int b, n, t, y, x;
-  __device__ __forceinline__ Place(const RopeArgs& A, int tok) {
-    b = A.by_n.div(tok);
-    n = tok - b * A.N;
-    t = A.by_hw.div(n);
-    const int r = n - t * A.HW;
-    y = A.by_w.div(r);
-    x = r - y * A.W;
-  }
-};
-
 // The angles of the group's tokens in shared memory: kSlots = D + 2 rows of up
 // to 64 (cos, sin).  Row r + D is fetched in iteration r over row r - 2, which
 // every thread of the group has left: all of them have met at a barrier of
@@ -81,9 +68,11 @@ struct Angles {
   // What this thread fetches: the pairs t and t + tpt (the second for d = 128 in one warp).
   const float2* src[2];
   int step[2], axis[2];
+  bool any;
   // What it reads: bit j of `turned` for the pair of channel j (halves) or 2j, 2j + 1; and for
   // halves the pair's place, the partner's place in the warp's scratch, and whether it is the second.
   uint32_t turned;
+  bool all;           // every channel of a head is turned: nothing to choose (grid-uniform)
   uint32_t at[HALVES ? 8 : 1];
   __device__ __forceinline__ static int place(int pair) { return HALVES ? pair + (pair >> 3) : pair; }
   __device__ __forceinline__ Angles(const RopeArgs& A, void* smem, const RowGroup& g, int ch0, int lph) {
@@ -105,6 +94,8 @@ struct Angles {
         base += n;
       }
     }
+    any = src[0] != nullptr || src[1] != nullptr;
+    all = A.dim[0] + A.dim[1] + A.dim[2] == A.d;
     turned = 0;
 #pragma unroll
     for (int j = 0; j < kN; ++j) {
@@ -117,11 +108,13 @@ struct Angles {
       }
     }
   }
-  __device__ __forceinline__ void fetch(const RowGroup& g, int slot, const Place& p) const {
+  __device__ __forceinline__ void fetch(const RopeArgs& A, const RowGroup& g, int slot, int n) const {
+    if (!any) return;
+    const int t = A.by_hw.div(n), r = n - t * A.HW, y = A.by_w.div(r), x = r - y * A.W;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       if (src[j] != nullptr) {
-        const int pos = axis[j] == 0 ? p.t : axis[j] == 1 ? p.y : p.x;
+        const int pos = axis[j] == 0 ? t : axis[j] == 1 ? y : x;
         cp_async8(smem_u32(rows + slot * kRow + place(g.t + j * g.tpt)), src[j] + (long long)pos * step[j]);
       }
     }
@@ -140,11 +133,14 @@ struct Angles {
       cs[3] = make_float2(b.z, b.w);
     }
   }
-  // v turned by +angle (dir = 1) or -angle (dir = -1); a channel that is not
+  // p turned by +angle (dir = 1) or -angle (dir = -1); a channel that is not
   // turned stays as it is, an infinity too.  `scratch`: this warp's 32 * 9
   // floats (a lane's 8 values at 9 * lane: no bank conflicts).
-  __device__ __forceinline__ void apply(float* v, const float2* cs, float dir, float* scratch, int lane) const {
+  __device__ __forceinline__ void apply(uint64_t* p, const float2* cs, float dir, float* scratch, int lane) const {
     if constexpr (HALVES) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f2_split(p[k], v[2 * k], v[2 * k + 1]);
       __syncwarp();
 #pragma unroll
       for (int j = 0; j < 8; ++j) scratch[lane * 9 + j] = v[j];
@@ -155,13 +151,16 @@ struct Angles {
         const float r = fmaf(v[j], cs[j].x, s * scratch[(at[j] >> 8) & 0x1ff]);
         v[j] = turned >> j & 1 ? r : v[j];
       }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) p[k] = f2(v[2 * k], v[2 * k + 1]);
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float a = v[2 * j], b = v[2 * j + 1], s = dir * cs[j].y;
-        const bool on = turned >> j & 1;
-        v[2 * j] = on ? fmaf(a, cs[j].x, -b * s) : a;
-        v[2 * j + 1] = on ? fmaf(a, s, b * cs[j].x) : b;
+        float a, b;
+        f2_split(p[j], a, b);
+        const float s = dir * cs[j].y;
+        const float ra = fmaf(a, cs[j].x, -b * s), rb = fmaf(a, s, b * cs[j].x);
+        p[j] = all || (turned >> j & 1) ? f2(ra, rb) : p[j];
       }
     }
   }
@@ -202,9 +201,9 @@ __global__ void __launch_bounds__(rope_bounds(CPT)) qkv_rope_kernel(const __grid
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(A.out[which]) + ch0;
     auto fetch = [&](int tok, int slot, int aslot) {
       if (tok < A.tokens) {
-        const Place at(A, tok);
-        if (which < 2) angles.fetch(g, aslot, at);
-        const T* row = in + at.b * sb + at.n * sn;
+        const int b = A.by_n.div(tok), n = tok - b * A.N;
+        if (which < 2) angles.fetch(A, g, aslot, n);
+        const T* row = in + b * sb + n * sn;
 #pragma unroll
         for (int i = 0; i < CPT; ++i)
           if (g.t + i * g.tpt < nchunk) ring.fetch(slot, i, row + (head0 + i * head_step) * sh);
@@ -213,24 +212,24 @@ __global__ void __launch_bounds__(rope_bounds(CPT)) qkv_rope_kernel(const __grid
     };
 #pragma unroll 1
     for (int s = 0; s < D; ++s) fetch(first + s * step, s, s);
-    float w[CPT][8];
+    uint64_t w[CPT][4];
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
       const int c = g.t + i * g.tpt;
-      if (norm != VEDA_NORM_NONE && c < nchunk) load8(A.w[which] + (norm == VEDA_NORM_ROW ? 8 * c : ch0), w[i]);
+      if (norm != VEDA_NORM_NONE && c < nchunk) load_pairs(A.w[which] + (norm == VEDA_NORM_ROW ? 8 * c : ch0), w[i]);
     }
     int slot = 0, aslot = 0;
     auto next = [](int s, int n) { return s + 1 == n ? 0 : s + 1; };
     for (int tok = first; tok < A.tokens; tok += step, flip ^= 1, slot = next(slot, D), aslot = next(aslot, D + 2)) {
       const int b = A.by_n.div(tok), n = tok - b * A.N;
-      float v[CPT][8];
+      uint64_t v[CPT][4];
       cp_async_wait<D - 1>();
 #pragma unroll
       for (int i = 0; i < CPT; ++i) {
-        ring.read(slot, i, v[i]);
+        to_pairs(ring.read(slot, i), v[i]);
         if (g.t + i * g.tpt >= nchunk) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) v[i][k] = 0.f;
+          for (int k = 0; k < 4; ++k) v[i][k] = 0;
         }
       }
       fetch(tok + D * step, slot, aslot >= 2 ? aslot - 2 : aslot + D);
@@ -240,9 +239,10 @@ __global__ void __launch_bounds__(rope_bounds(CPT)) qkv_rope_kernel(const __grid
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < CPT; ++i) {
-          r[i] = 0.f;
+          uint64_t s2 = 0;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) r[i] = fmaf(v[i][k], v[i][k], r[i]);
+          for (int k = 0; k < 4; ++k) s2 = f2_fma(v[i][k], v[i][k], s2);
+          r[i] = f2_sum(s2);
           ss += r[i];
         }
         if (norm == VEDA_NORM_ROW) {
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(rope_bounds(CPT)) qkv_rope_kernel(const __grid
         for (int i = 0; i < CPT; ++i) {
           if (g.t + i * g.tpt < nchunk) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[i][k] *= r[i] * w[i][k];
+            for (int k = 0; k < 4; ++k) v[i][k] = f2_mul(f2_mul(v[i][k], f2_all(r[i])), w[i][k]);
           }
         }
       }
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(rope_bounds(CPT)) qkv_rope_kernel(const __grid
         const int head = head0 + i * head_step;
         if (which < 2) angles.apply(v[i], cs, 1.f, scratch, g.lane);
         if (g.t + i * g.tpt < nchunk && VEDA_IN_BOUNDS(head < A.heads && tok < A.tokens))
-          store8(out + (row + (long long)head * A.N) * A.d, v[i]);
+          store_pairs(out + (row + (long long)head * A.N) * A.d, v[i]);
       }
     }
   }
@@ -302,15 +302,15 @@ __global__ void __launch_bounds__(512) qkv_rope_bwd_kernel(const __grid_constant
     const long long dsb = A.dsb[which], dsn = A.dsn[which], dsh = A.dsh[which];
     auto fetch = [&](int tok, int slot, int aslot) {
       if (tok < A.tokens) {
-        const Place at(A, tok);
-        if (which < 2) angles.fetch(g, aslot, at);
-        const long long row = (long long)at.b * A.heads * A.N + at.n;
+        const int b = A.by_n.div(tok), n = tok - b * A.N;
+        if (which < 2) angles.fetch(A, g, aslot, n);
+        const long long row = (long long)b * A.heads * A.N + n;
 #pragma unroll
         for (int i = 0; i < CPT; ++i) {
           const int head = head0 + i * head_step;
           if (g.t + i * g.tpt < nchunk) {
             rg.fetch(slot, i, dout + (row + (long long)head * A.N) * A.d);
-            if (norm != VEDA_NORM_NONE) rx.fetch(slot, i, in + at.b * sb + at.n * sn + head * sh);
+            if (norm != VEDA_NORM_NONE) rx.fetch(slot, i, in + b * sb + n * sn + head * sh);
           }
         }
       }
@@ -318,27 +318,27 @@ __global__ void __launch_bounds__(512) qkv_rope_bwd_kernel(const __grid_constant
     };
 #pragma unroll 1
     for (int s = 0; s < D; ++s) fetch(first + s * step, s, s);
-    float w[CPT][8], acc[CPT][8];
+    uint64_t w[CPT][4], acc[CPT][4];
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
       const int c = g.t + i * g.tpt;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) acc[i][k] = w[i][k] = 0.f;
-      if (norm != VEDA_NORM_NONE && c < nchunk) load8(A.w[which] + (norm == VEDA_NORM_ROW ? 8 * c : ch0), w[i]);
+      for (int k = 0; k < 4; ++k) acc[i][k] = w[i][k] = 0;
+      if (norm != VEDA_NORM_NONE && c < nchunk) load_pairs(A.w[which] + (norm == VEDA_NORM_ROW ? 8 * c : ch0), w[i]);
     }
     int slot = 0, aslot = 0;
     auto next = [](int s, int n) { return s + 1 == n ? 0 : s + 1; };
     for (int tok = first; tok < A.tokens; tok += step, flip ^= 1, slot = next(slot, D), aslot = next(aslot, D + 2)) {
       const int b = A.by_n.div(tok), n = tok - b * A.N;
-      float gv[CPT][8], v[CPT][8];
+      uint64_t gv[CPT][4], v[CPT][4];
       cp_async_wait<D - 1>();
 #pragma unroll
       for (int i = 0; i < CPT; ++i) {
-        rg.read(slot, i, gv[i]);
-        if (norm != VEDA_NORM_NONE) rx.read(slot, i, v[i]);
+        to_pairs(rg.read(slot, i), gv[i]);
+        if (norm != VEDA_NORM_NONE) to_pairs(rx.read(slot, i), v[i]);
         if (g.t + i * g.tpt >= nchunk) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) gv[i][k] = v[i][k] = 0.f;
+          for (int k = 0; k < 4; ++k) gv[i][k] = v[i][k] = 0;
         }
       }
       fetch(tok + D * step, slot, aslot >= 2 ? aslot - 2 : aslot + D);
@@ -353,12 +353,14 @@ __global__ void __launch_bounds__(512) qkv_rope_bwd_kernel(const __grid_constant
         float s1[CPT], s2[CPT];
 #pragma unroll
         for (int i = 0; i < CPT; ++i) {
-          s1[i] = s2[i] = 0.f;
+          uint64_t p1 = 0, p2 = 0;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            s1[i] = fmaf(v[i][k], v[i][k], s1[i]);
-            s2[i] = fmaf(gv[i][k] * w[i][k], v[i][k], s2[i]);
+          for (int k = 0; k < 4; ++k) {
+            p1 = f2_fma(v[i][k], v[i][k], p1);
+            p2 = f2_fma(f2_mul(gv[i][k], w[i][k]), v[i][k], p2);
           }
+          s1[i] = f2_sum(p1);
+          s2[i] = f2_sum(p2);
         }
         if (norm == VEDA_NORM_ROW) {
           float a = 0.f, c = 0.f;
@@ -373,11 +375,12 @@ __global__ void __launch_bounds__(512) qkv_rope_bwd_kernel(const __grid_constant
         }
 #pragma unroll
         for (int i = 0; i < CPT; ++i) {
-          const float rstd = rsqrtf(s1[i] * A.inv_n + A.eps), c1 = s2[i] * A.inv_n * rstd * rstd;
+          const float rstd = rsqrtf(s1[i] * A.inv_n + A.eps);
+          const uint64_t rr = f2_all(rstd), cc = f2_all(-s2[i] * A.inv_n * rstd * rstd);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            acc[i][k] = fmaf(gv[i][k] * rstd, v[i][k], acc[i][k]);
-            gv[i][k] = rstd * (gv[i][k] * w[i][k] - v[i][k] * c1);
+          for (int k = 0; k < 4; ++k) {
+            acc[i][k] = f2_fma(f2_mul(gv[i][k], rr), v[i][k], acc[i][k]);
+            gv[i][k] = f2_mul(rr, f2_fma(v[i][k], cc, f2_mul(gv[i][k], w[i][k])));
           }
         }
       }
@@ -385,7 +388,7 @@ __global__ void __launch_bounds__(512) qkv_rope_bwd_kernel(const __grid_constant
       for (int i = 0; i < CPT; ++i) {
         const int head = head0 + i * head_step;
         if (g.t + i * g.tpt < nchunk && VEDA_IN_BOUNDS(head < A.heads && tok < A.tokens))
-          store8(dx + b * dsb + n * dsn + head * dsh, gv[i]);
+          store_pairs(dx + b * dsb + n * dsn + head * dsh, gv[i]);
       }
     }
     float* part = A.part[which];
@@ -402,15 +405,15 @@ __global__ void __launch_bounds__(512) qkv_rope_bwd_kernel(const __grid_constant
 #pragma unroll
       for (int i = 0; i < CPT; ++i) {
         const int c = g.t + i * g.tpt;
-        if (c < nchunk) store8(sums + g.group * C + 8 * c, acc[i]);
+        if (c < nchunk) store_pairs(sums + g.group * C + 8 * c, acc[i]);
       }
     } else {
 #pragma unroll
       for (int i = 1; i < CPT; ++i) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) acc[0][k] += acc[i][k];
+        for (int k = 0; k < 4; ++k) acc[0][k] = f2_add(acc[0][k], acc[i][k]);
       }
-      store8(sums + (threadIdx.x / lph) * C + ch0, acc[0]);
+      store_pairs(sums + (threadIdx.x / lph) * C + ch0, acc[0]);
     }
     __syncthreads();
     for (int c = threadIdx.x; c < C; c += blockDim.x) {

@@ -23,31 +23,34 @@ template <typename T>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const __grid_constant__ QuantArgs A) {
   const int blocks = (A.C + 127) / 128;
   const int kb = blockIdx.x % blocks;
-  const long long r0 = (long long)(blockIdx.x / blocks) * kQuantRows + (threadIdx.x >> 4);
+  const int r0 = blockIdx.x / blocks * kQuantRows + (threadIdx.x >> 4);
   const int l = threadIdx.x & 15;
   const int c = kb * 128 + l * 8;
   const bool in_c = c < A.C;
   const T* x = static_cast<const T*>(A.x) + (in_c ? (c / A.d) * A.sh + c % A.d : 0);
-  float v[4][8];
+  Words<T> w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const long long row = r0 + 16 * i;
-    if (in_c && row < A.rows) load8(x + row / A.N * A.sb + row % A.N * A.sn, v[i]);
+    const int row = r0 + 16 * i;
+    if (in_c && row < A.rows) {
+      const int b = A.by_n.div(row), n = row - b * (int)A.N;
+      const uint4* p = reinterpret_cast<const uint4*>(x + b * A.sb + n * A.sn);
+#pragma unroll
+      for (int k = 0; k < (int)(sizeof(T) / 2); ++k) w[i].u[k] = __ldcs(p + k);
+    }
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const long long row = r0 + 16 * i;
+    const int row = r0 + 16 * i;
     const bool here = in_c && row < A.rows;
-    uint32_t m = kTinyBits;
-    if (here) {
+    uint64_t v[4];
+    to_pairs(w[i], v);
+    float a = kTiny;
+    if (here) a = max_abs(a, v);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) m = max(m, abs_bits(v[i][k]));
-    }
-#pragma unroll
-    for (int off = 8; off; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
-    const float a = __uint_as_float(m);
+    for (int off = 8; off; off >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, off));
     if (here && VEDA_IN_BOUNDS(row < A.rows && c + 8 <= A.C)) {
-      *reinterpret_cast<uint2*>(A.q + row * A.C + c) = pack_e4m3x8(v[i], kE4M3Max / a);
+      *reinterpret_cast<uint2*>(A.q + (long long)row * A.C + c) = to_e4m3(v, kE4M3Max / a);
       if (l == 0) A.scale[kb * A.rows + row] = a / kE4M3Max;
     }
   }
@@ -57,36 +60,37 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const __grid_constant__
 template <typename T>
 __global__ void __launch_bounds__(256) quant_weight_kernel(const T* __restrict__ w, int N, int K, uint8_t* q,
                                                            float* scale) {
-  __shared__ uint32_t red[8];
+  __shared__ float red[8];
   const int kbs = (K + 127) / 128, nb = blockIdx.x / kbs, kb = blockIdx.x % kbs;
   const int c = kb * 128 + (threadIdx.x & 15) * 8, n0 = nb * 128 + (threadIdx.x >> 4);
-  float v[8][8];
-  uint32_t m = kTinyBits;
+  uint64_t v[8][4];
+  float a = kTiny;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int n = n0 + 16 * i;
     if (n < N && c < K) {
-      load8(w + (long long)n * K + c, v[i]);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) m = max(m, abs_bits(v[i][k]));
+      load_pairs(w + (long long)n * K + c, v[i]);
+      a = max_abs(a, v[i]);
     }
   }
-  m = __reduce_max_sync(0xffffffffu, m);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+#pragma unroll
+  for (int off = 16; off; off >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, off));
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = a;
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < 8; ++k) m = max(m, red[k]);
-  const float a = __uint_as_float(m), r = kE4M3Max / a;
+  for (int k = 0; k < 8; ++k) a = max_nan(a, red[k]);
+  const float r = kE4M3Max / a;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int n = n0 + 16 * i;
     if (n < N && c < K && VEDA_IN_BOUNDS(c + 8 <= K))
-      *reinterpret_cast<uint2*>(q + (long long)n * K + c) = pack_e4m3x8(v[i], r);
+      *reinterpret_cast<uint2*>(q + (long long)n * K + c) = to_e4m3(v[i], r);
   }
   if (threadIdx.x == 0) scale[blockIdx.x] = a / kE4M3Max;
 }
 
-cudaError_t launch_quant_rows(const QuantArgs& a, int type, cudaStream_t s) {
+cudaError_t launch_quant_rows(QuantArgs a, int type, cudaStream_t s) {
+  a.by_n = FastDiv((uint32_t)a.N);
   const long long grid = (a.rows + kQuantRows - 1) / kQuantRows * ((a.C + 127) / 128);
   if (type == VEDA_BF16) quant_rows_kernel<__nv_bfloat16><<<(unsigned)grid, 256, 0, s>>>(a);
   else if (type == VEDA_FP16) quant_rows_kernel<__half><<<(unsigned)grid, 256, 0, s>>>(a);

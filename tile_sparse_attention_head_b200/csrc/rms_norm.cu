@@ -43,11 +43,11 @@ __global__ void __launch_bounds__(512) add_rms_norm_kernel(const __grid_constant
   const TX* x = static_cast<const TX*>(A.x) + 8 * g.t;
   const TD* delta = A.delta == nullptr ? nullptr : static_cast<const TD*>(A.delta) + 8 * g.t;
   TX* h = static_cast<TX*>(A.h);
-  float w[CPT][8];
+  uint64_t w[CPT][4];
 #pragma unroll
   for (int i = 0; i < CPT; ++i) {
     const int c = g.t + i * g.tpt;
-    if (c < nchunk) load8(A.w + 8 * c, w[i]);
+    if (c < nchunk) load_pairs(A.w + 8 * c, w[i]);
   }
   const float inv_c = 1.f / (float)A.C;
   const long long step = (long long)gridDim.x * g.groups;
@@ -67,55 +67,46 @@ __global__ void __launch_bounds__(512) add_rms_norm_kernel(const __grid_constant
 #pragma unroll 1
   for (int s = 0; s < D; ++s) fetch(row + s * step, s);
   for (int turn = 0, slot = 0; row < A.rows; row += step, turn ^= 1, slot = slot + 1 == D ? 0 : slot + 1) {
-    float v[CPT][8];
+    Words<TX> hw[CPT];
     cp_async_wait<D - 1>();
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
-      rx.read(slot, i, v[i]);
-      if (delta != nullptr) {
-        float d[8];
-        rd.read(slot, i, d);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[i][k] = round_to<TX>(v[i][k] + d[k]);
-      }
+      hw[i] = rx.read(slot, i);
+      if (delta != nullptr) add_to(hw[i], rd.read(slot, i));
     }
     fetch(row + D * step, slot);
-    float ss = 0.f;
+    uint64_t v[CPT][4];
+    uint64_t ss = 0;
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
       const int c = g.t + i * g.tpt;
+      to_pairs(hw[i], v[i]);
       if (c < nchunk) {
-        if (h != nullptr && VEDA_IN_BOUNDS(row < A.rows)) store8(h + row * A.C + 8 * c, v[i]);
+        if (h != nullptr && VEDA_IN_BOUNDS(row < A.rows)) store_words(h + row * A.C + 8 * c, hw[i]);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) ss = fmaf(v[i][k], v[i][k], ss);
+        for (int k = 0; k < 4; ++k) ss = f2_fma(v[i][k], v[i][k], ss);
       }
     }
-    const float rstd = rsqrtf(row_sum(g, ss, red, turn) * inv_c + A.eps);
+    const float rstd = rsqrtf(row_sum(g, f2_sum(ss), red, turn) * inv_c + A.eps);
     if (A.rstd != nullptr && g.t == 0) A.rstd[row] = rstd;
+    const uint64_t rr = f2_all(rstd);
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
       const int c = g.t + i * g.tpt;
-      float y[8];
-      if (c < nchunk) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] = v[i][k] * rstd * w[i][k];
-      }
+      for (int k = 0; k < 4; ++k) v[i][k] = f2_mul(f2_mul(v[i][k], rr), w[i][k]);
       if constexpr (FP8) {
         // Chunks c .. c+15 of an aligned half-warp are one block of 128 channels.
-        uint32_t m = kTinyBits;
-        if (c < nchunk) {
+        float a = kTiny;
+        if (c < nchunk) a = max_abs(a, v[i]);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) m = max(m, abs_bits(y[k]));
-        }
-#pragma unroll
-        for (int off = 8; off; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
-        const float a = __uint_as_float(m);
+        for (int off = 8; off; off >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, off));
         if (c < nchunk) {
-          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(A.y) + row * A.C + 8 * c) = pack_e4m3x8(y, kE4M3Max / a);
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(A.y) + row * A.C + 8 * c) = to_e4m3(v[i], kE4M3Max / a);
           if ((c & 15) == 0) A.scale[(long long)(c >> 4) * A.rows + row] = a / kE4M3Max;
         }
       } else {
-        if (c < nchunk) store8(static_cast<TD*>(A.y) + row * A.C + 8 * c, y);
+        if (c < nchunk) store_pairs(static_cast<TD*>(A.y) + row * A.C + 8 * c, v[i]);
       }
     }
   }
@@ -133,13 +124,13 @@ __global__ void __launch_bounds__(512) add_rms_norm_bwd_kernel(const __grid_cons
   const TX* h = static_cast<const TX*>(A.h) + 8 * g.t;
   const TX* dh = A.dh == nullptr ? nullptr : static_cast<const TX*>(A.dh) + 8 * g.t;
   const TD* dy = static_cast<const TD*>(A.dy) + 8 * g.t;
-  float w[CPT][8], acc[CPT][8];
+  uint64_t w[CPT][4], acc[CPT][4];
 #pragma unroll
   for (int i = 0; i < CPT; ++i) {
     const int c = g.t + i * g.tpt;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) acc[i][k] = 0.f;
-    if (c < nchunk) load8(A.w + 8 * c, w[i]);
+    for (int k = 0; k < 4; ++k) acc[i][k] = 0;
+    if (c < nchunk) load_pairs(A.w + 8 * c, w[i]);
   }
   const float inv_c = 1.f / (float)A.C;
   const long long step = (long long)gridDim.x * g.groups;
@@ -162,45 +153,44 @@ __global__ void __launch_bounds__(512) add_rms_norm_bwd_kernel(const __grid_cons
   for (int s = 0; s < D; ++s) fetch(row + s * step, s);
   float nrstd = row < A.rows ? A.rstd[row] : 0.f;
   for (int turn = 0, slot = 0; row < A.rows; row += step, turn ^= 1, slot = slot + 1 == D ? 0 : slot + 1) {
-    float hv[CPT][8], gv[CPT][8], dv[CPT][8];
-    float s = 0.f;
+    uint64_t hv[CPT][4], gv[CPT][4];
+    Words<TX> dv[CPT];
     const float rstd = nrstd;
     cp_async_wait<D - 1>();
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
-      rh.read(slot, i, hv[i]);
-      rdy.read(slot, i, gv[i]);
-      if (dh != nullptr) {
-        rdh.read(slot, i, dv[i]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) dv[i][k] = 0.f;
-      }
+      to_pairs(rh.read(slot, i), hv[i]);
+      to_pairs(rdy.read(slot, i), gv[i]);
+      if (dh != nullptr) dv[i] = rdh.read(slot, i);
     }
     fetch(row + D * step, slot);
     if (row + step < A.rows) nrstd = A.rstd[row + step];
+    const uint64_t rr = f2_all(rstd);
+    uint64_t ss = 0;
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
       if (g.t + i * g.tpt < nchunk) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          acc[i][k] = fmaf(gv[i][k] * rstd, hv[i][k], acc[i][k]);
-          gv[i][k] *= w[i][k];
-          s = fmaf(gv[i][k], hv[i][k], s);
+        for (int k = 0; k < 4; ++k) {
+          acc[i][k] = f2_fma(f2_mul(gv[i][k], rr), hv[i][k], acc[i][k]);
+          gv[i][k] = f2_mul(gv[i][k], w[i][k]);
+          ss = f2_fma(gv[i][k], hv[i][k], ss);
         }
       }
     }
-    s = row_sum(g, s, red, turn);
-    const float c1 = s * inv_c * rstd * rstd;
+    const float c1 = -row_sum(g, f2_sum(ss), red, turn) * inv_c * rstd * rstd;
+    const uint64_t cc = f2_all(c1);
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
       const int c = g.t + i * g.tpt;
       if (c < nchunk) {
+        uint64_t d[4] = {0, 0, 0, 0};
+        if (dh != nullptr) to_pairs(dv[i], d);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) dv[i][k] = fmaf(rstd, gv[i][k] - hv[i][k] * c1, dv[i][k]);
+        for (int k = 0; k < 4; ++k) d[k] = f2_fma(rr, f2_fma(hv[i][k], cc, gv[i][k]), d[k]);
         if (VEDA_IN_BOUNDS(row < A.rows)) {
-          if (A.dx != nullptr) store8(static_cast<TX*>(A.dx) + row * A.C + 8 * c, dv[i]);
-          if (A.ddelta != nullptr) store8(static_cast<TD*>(A.ddelta) + row * A.C + 8 * c, dv[i]);
+          if (A.dx != nullptr) store_pairs(static_cast<TX*>(A.dx) + row * A.C + 8 * c, d);
+          if (A.ddelta != nullptr) store_pairs(static_cast<TD*>(A.ddelta) + row * A.C + 8 * c, d);
         }
       }
     }
@@ -212,7 +202,7 @@ __global__ void __launch_bounds__(512) add_rms_norm_bwd_kernel(const __grid_cons
 #pragma unroll
   for (int i = 0; i < CPT; ++i) {
     const int c = g.t + i * g.tpt;
-    if (c < nchunk) store8(sums + g.group * A.C + 8 * c, acc[i]);
+    if (c < nchunk) store_pairs(sums + g.group * A.C + 8 * c, acc[i]);
   }
   __syncthreads();
   for (int c = threadIdx.x; c < A.C; c += blockDim.x) {
