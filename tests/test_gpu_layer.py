@@ -246,16 +246,9 @@ def test_add_rms_norm_fp8(V, rows, C, tx, td):
     check_blocks(q, s, L.rms_norm(f64(h), f64(w), 1e-6)[0], "fp8 norm")
 
 
-def torch_blocks(x):
-    """The rule in fp32, elementwise operations only: the kernel's values have to be equal.  (Divisions are of
-    tensors by tensors: with a Python number torch multiplies by a rounded reciprocal.)"""
-    rows, C = x.shape
-    blocks = -(-C // 128)
-    xp = torch.nn.functional.pad(x.float(), (0, blocks * 128 - C)).view(rows, blocks, 128)
-    a = xp.abs().amax(-1).clamp_min(2.0 ** -100)
-    top = torch.full_like(a, 448.0)
-    q = (xp * (top / a)[..., None]).to(FP8).view(rows, -1)[:, :C]
-    return q, (a / top).t()
+# A scale is one rounding of a / 448 and of 1 / 448 away from exact, its reciprocal two units more, the product one
+# rounding: 2^-21 in all.
+QUANT_REL = 2.0 ** -21
 
 
 @pytest.mark.parametrize("t", [BF16, FP16, FP32])
@@ -264,8 +257,7 @@ def test_quant_fp8(V, rows, C, t):
     x = (rand(rows, C) * torch.exp(2 * rand(rows, 1, seed=1))).to(t)
     x[0, :] = 0
     q, s = V.quant_fp8(x)
-    rq, rs = torch_blocks(x)
-    assert torch.equal(q.view(torch.uint8), rq.contiguous().view(torch.uint8)) and torch.equal(s, rs)
+    check_blocks(q, s, f64(x), "quant", rel=QUANT_REL)
     wide = torch.zeros(rows, C + 24, dtype=t, device="cuda")
     wide[:, 8:8 + C] = x
     q2, s2 = V.quant_fp8(wide[:, 8:8 + C])
@@ -276,8 +268,7 @@ def test_quant_fp8(V, rows, C, t):
 def test_quant_fp8_heads(V, B, heads, N, d):
     o = rand(B, heads, N, d, t=BF16)
     q, s = V.quant_fp8_heads(o)
-    rq, rs = torch_blocks(o.transpose(1, 2).reshape(B * N, heads * d))
-    assert torch.equal(q.view(torch.uint8), rq.contiguous().view(torch.uint8)) and torch.equal(s, rs)
+    check_blocks(q, s, f64(o.transpose(1, 2).reshape(B * N, heads * d)), "quant heads", rel=QUANT_REL)
     t = o.transpose(1, 2).contiguous().transpose(1, 2)      # token order behind the same shape
     q2, s2 = V.quant_fp8_heads(t)
     assert torch.equal(q2.view(torch.uint8), q.view(torch.uint8)) and torch.equal(s2, s)
@@ -304,10 +295,10 @@ def test_quant_fp8_weight(V, N, K, t):
     for i in range(0, N, 128):
         for j in range(0, K, 128):
             b = w[i:i + 128, j:j + 128]
-            a = b.abs().max()
-            top = torch.full_like(a, 448.0)
-            assert s[i // 128, j // 128] == a / top
-            assert torch.equal(q[i:i + 128, j:j + 128].float(), (b * (top / a)).to(FP8).float())
+            ref = max(float(b.abs().max()), L.TINY) / 448
+            assert abs(float(s[i // 128, j // 128]) - ref) <= QUANT_REL * ref
+            v = f64(b) / ref
+            close(f64(q[i:i + 128, j:j + 128].float()), v, FP8, np.abs(v), rel=QUANT_REL, what="weight")
 
 
 def gemm_inputs(M, K, N, seed=0):

@@ -80,13 +80,24 @@ __device__ __forceinline__ void load_pairs(const T* p, uint64_t* v) {
   for (int k = 0; k < (int)(sizeof(T) / 2); ++k) w.u[k] = reinterpret_cast<const uint4*>(p)[k];
   to_pairs(w, v);
 }
+// One store per chunk: two of 16 bytes would each touch half of every sector.
 template <typename T>
 __device__ __forceinline__ void store_words(T* p, const Words<T>& w) {
-#pragma unroll
-  for (int k = 0; k < (int)(sizeof(T) / 2); ++k) reinterpret_cast<uint4*>(p)[k] = w.u[k];
+  if constexpr (sizeof(T) == 4) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w.u[0].x), "r"(w.u[0].y),
+                 "r"(w.u[0].z), "r"(w.u[0].w), "r"(w.u[1].x), "r"(w.u[1].y), "r"(w.u[1].z), "r"(w.u[1].w));
+  } else {
+    *reinterpret_cast<uint4*>(p) = w.u[0];
+  }
 }
 template <typename T>
 __device__ __forceinline__ void store_pairs(T* p, const uint64_t* v) { store_words(p, to_words<T>(v)); }
+
+__device__ __forceinline__ void store_shared(float* p, const uint64_t* v) {
+  const Words<float> w = to_words<float>(v);
+  reinterpret_cast<uint4*>(p)[0] = w.u[0];
+  reinterpret_cast<uint4*>(p)[1] = w.u[1];
+}
 
 // x + d rounded to x's type.  Of two 16-bit values the sum is exact in fp32, or
 // so far from a rounding border that one rounding and two agree, so the 16-bit
@@ -131,10 +142,13 @@ __device__ __forceinline__ float f2_sum(uint64_t a) {
 }
 
 // Chunks on their way from global memory, D rows ahead of their use, in shared
-// memory.  A thread copies (cp.async, 16 bytes at a time) and reads its own
-// chunks only, so nothing has to be synchronised between threads: one commit
-// per row, and a wait for all but the D - 1 newest rows before reading.  The
-// layout is [slot][chunk][16-byte piece][thread]: no bank conflicts.
+// memory.  A warp copies (cp.async, 16 bytes at a time) and reads its own
+// chunks only, so no barrier is needed: one commit per row, and a wait for all
+// but the D - 1 newest rows before reading.  A 16-bit chunk is one piece, which
+// its thread copies itself.  An fp32 chunk is two; there lane l copies the
+// pieces l and 32 + l of the warp's 64, so that a copy's sectors are whole, and
+// the warp synchronises around it.  Piece q lies at q ^ (q / 8 & 1), which
+// leaves no bank conflicts.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -147,24 +161,65 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+//
+// A slot is named by its first chunk's place, slot * CPT * blockDim.x.
 template <typename T, int CPT>
 struct Ring {
   static constexpr int kPieces = sizeof(T) / 2;
   static constexpr int kBytes = CPT * kPieces * 16;   // per thread and slot
-  const uint4* base;
-  __device__ __forceinline__ explicit Ring(const void* smem) : base(static_cast<const uint4*>(smem) + threadIdx.x) {}
-  __device__ __forceinline__ const uint4* at(int slot, int i, int k) const {
-    return base + ((slot * CPT + i) * kPieces + k) * blockDim.x;
-  }
-  __device__ __forceinline__ void fetch(int slot, int i, const T* p) const {
+  const uint4* mine;                                  // the warp's part of slot 0, chunk 0
+  uint32_t write[kPieces];
+  int threads;
+  __device__ __forceinline__ explicit Ring(const void* smem) : threads(blockDim.x) {
+    const int lane = threadIdx.x & 31;
+    mine = static_cast<const uint4*>(smem) + (threadIdx.x - lane) * kPieces;
 #pragma unroll
-    for (int k = 0; k < kPieces; ++k) cp_async16(smem_u32(at(slot, i, k)), reinterpret_cast<const uint4*>(p) + k);
+    for (int j = 0; j < kPieces; ++j) write[j] = smem_u32(mine + place(lane + 32 * j));
+  }
+  __device__ __forceinline__ static int place(int q) { return kPieces == 1 ? q : q ^ (q >> 3 & 1); }
+  // The chunk, relative to the thread's own, that its piece j belongs to, and the piece's first channel there.
+  __device__ __forceinline__ static int other(int j) {
+    const int lane = threadIdx.x & 31;
+    return kPieces == 1 ? 0 : ((lane + 32 * j) >> 1) - lane;
+  }
+  __device__ __forceinline__ static int channel(int j) { return kPieces == 1 ? 0 : (threadIdx.x & 1) * 4; }
+  __device__ __forceinline__ void fetch(int slot, int i, int j, const T* p) const {
+    cp_async16(write[j] + (slot + i * threads) * (kPieces * 16), p);
   }
   __device__ __forceinline__ Words<T> read(int slot, int i) const {
     Words<T> w;
 #pragma unroll
-    for (int k = 0; k < kPieces; ++k) w.u[k] = *at(slot, i, k);
+    for (int j = 0; j < kPieces; ++j)
+      w.u[j] = mine[(slot + i * threads) * kPieces + place(kPieces * (threadIdx.x & 31) + j)];
     return w;
+  }
+  // Around the reads of a row: its pieces have come, and may be overwritten.
+  __device__ __forceinline__ static void sync() {
+    if constexpr (kPieces == 2) __syncwarp();
+  }
+};
+
+// The pieces that a thread copies of a dense row, as offsets (in elements) from the row's start.
+template <typename T, int CPT>
+struct RowPieces {
+  static constexpr int kPieces = sizeof(T) / 2;
+  int off[kPieces], step, valid;
+  __device__ __forceinline__ RowPieces(int t, int tpt, int nchunk) : step(8 * tpt), valid(0) {
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      const int c = t + Ring<T, CPT>::other(j);
+      off[j] = 8 * c + Ring<T, CPT>::channel(j);
+#pragma unroll
+      for (int i = 0; i < CPT; ++i) valid |= (c + i * tpt < nchunk ? 1 : 0) << (i * kPieces + j);
+    }
+  }
+  __device__ __forceinline__ void fetch(const Ring<T, CPT>& ring, int slot, const T* row) const {
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j)
+        if (valid >> (i * kPieces + j) & 1) ring.fetch(slot, i, j, row + (off[j] + i * step));
+    }
   }
 };
 
@@ -180,9 +235,9 @@ __device__ __forceinline__ float warp_sum(float v) {
 struct RowSplit {
   int cpt, W, groups, threads;
 };
-inline RowSplit row_split(int nchunk, long long rows, int sms) {
+inline RowSplit row_split(int nchunk, long long rows, int sms, int most_for_two = 1024) {
   RowSplit r;
-  r.cpt = nchunk <= 32 ? 1 : nchunk <= 1024 ? 2 : 4;
+  r.cpt = nchunk <= 32 ? 1 : nchunk <= most_for_two ? 2 : 4;
   r.W = (nchunk + 32 * r.cpt - 1) / (32 * r.cpt);
   r.groups = 16 / r.W;
   const long long each = (rows + sms - 1) / sms;   // few rows: spread them over the SMs first
@@ -252,12 +307,21 @@ inline unsigned resident_ctas(K kernel, int threads, size_t smem, int sms) {
 }
 
 // The 8-bit rule: a block's scale is s = a / 448 with a its largest magnitude,
-// but at least 2^-100 (so that a block of zeros has a scale and 448 / a stays
-// finite), and the block holds e4m3(x * (448 / a)), nearest even.  The maximum
+// but at least 2^-100 (so that a block of zeros has a scale and 1 / s stays
+// finite), and the block holds e4m3(x / s), nearest even.  Both quotients are
+// products with a reciprocal, to fp32's last places: a division's full
+// sequence, twice per 8 channels, was a fifth of the instructions.  The maximum
 // passes NaN on: a block with an infinity or NaN gets a scale that is infinite
 // or NaN, and stands for NaN as a whole, rather than for a finite wrong value.
-constexpr float kE4M3Max = 448.f;
 constexpr float kTiny = 7.888609052210118e-31f;   // 2^-100
+
+__device__ __forceinline__ float e4m3_scale(float a) { return a * (1.f / 448.f); }
+// Of a scale: between 2^-109 and 2^120, so its reciprocal is a normal number.
+__device__ __forceinline__ float reciprocal(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return r;
+}
 
 __device__ __forceinline__ float max_nan(float a, float b) {
   float d;

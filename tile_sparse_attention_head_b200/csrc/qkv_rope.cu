@@ -153,16 +153,20 @@ struct Angles {
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) p[k] = f2(v[2 * k], v[2 * k + 1]);
+    } else if (all) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) p[j] = turn(p[j], cs[j].x, dir * cs[j].y);
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        float a, b;
-        f2_split(p[j], a, b);
-        const float s = dir * cs[j].y;
-        const float ra = fmaf(a, cs[j].x, -b * s), rb = fmaf(a, s, b * cs[j].x);
-        p[j] = all || (turned >> j & 1) ? f2(ra, rb) : p[j];
+        if (turned >> j & 1) p[j] = turn(p[j], cs[j].x, dir * cs[j].y);
       }
     }
+  }
+  __device__ __forceinline__ static uint64_t turn(uint64_t p, float c, float s) {
+    float a, b;
+    f2_split(p, a, b);
+    return f2(fmaf(a, c, -b * s), fmaf(a, s, b * c));
   }
 };
 
@@ -172,11 +176,25 @@ __device__ __forceinline__ float head_sum(float v, int lanes) {
 }
 
 // Rows in flight per group, and the thread count that register use is bounded
-// by: two CTAs of up to 10 warps (or of 512 threads with one chunk each) are to
-// fit an SM.
+// by: 20 warps are to fit an SM, 32 with one chunk each.
 __host__ __device__ constexpr int rope_bounds(int cpt) { return cpt == 1 ? 1024 : cpt == 2 ? 640 : 512; }
-__host__ __device__ constexpr int rope_depth(int cpt) { return cpt == 4 ? 2 : 4; }
+__host__ __device__ constexpr int rope_depth(int cpt) { return cpt == 4 ? 3 : 4; }
 __host__ __device__ constexpr int rope_bwd_depth(int cpt) { return cpt == 4 ? 1 : 3; }
+
+// A token's row on its way: chunk c of it starts at (c / lph) * sh + c % lph * 8.
+template <typename T, int CPT>
+__device__ __forceinline__ void fetch_token(const RopeArgs& A, const Ring<T, CPT>& ring, int slot, const RowGroup& g,
+                                            int nchunk, int lph, const T* row, long long sh) {
+  const int shift = lph == 16 ? 4 : 3;
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) {
+#pragma unroll
+    for (int j = 0; j < Ring<T, CPT>::kPieces; ++j) {
+      const int c = g.t + i * g.tpt + ring.other(j);
+      if (c < nchunk) ring.fetch(slot, i, j, row + (c >> shift) * sh + ((c & (lph - 1)) * 8 + ring.channel(j)));
+    }
+  }
+}
 
 template <typename T, int CPT, bool HALVES>
 __global__ void __launch_bounds__(rope_bounds(CPT)) qkv_rope_kernel(const __grid_constant__ RopeArgs A) {
@@ -190,28 +208,26 @@ __global__ void __launch_bounds__(rope_bounds(CPT)) qkv_rope_kernel(const __grid
   const int lph = A.d / 8, nchunk = A.heads * lph;
   const int ch0 = (g.t % lph) * 8, head0 = g.t / lph, head_step = g.tpt / lph;
   const int step = gridDim.x * g.groups, first = blockIdx.x * g.groups + g.group;
+  const int slot_size = CPT * blockDim.x;
   const Angles<HALVES, D> angles(A, rest, g, ch0, lph);
   int flip = 0;
   for (int o = 0; o < A.n_order; ++o) {
     if (o > 0) __syncthreads();   // the angles' slots start over
     const int which = A.order[o];
     const int norm = which == 2 ? VEDA_NORM_NONE : A.norm;
-    const T* in = static_cast<const T*>(A.in[which]) + ch0;
+    const T* in = static_cast<const T*>(A.in[which]);
     const long long sb = A.sb[which], sn = A.sn[which], sh = A.sh[which];
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(A.out[which]) + ch0;
     auto fetch = [&](int tok, int slot, int aslot) {
       if (tok < A.tokens) {
         const int b = A.by_n.div(tok), n = tok - b * A.N;
         if (which < 2) angles.fetch(A, g, aslot, n);
-        const T* row = in + b * sb + n * sn;
-#pragma unroll
-        for (int i = 0; i < CPT; ++i)
-          if (g.t + i * g.tpt < nchunk) ring.fetch(slot, i, row + (head0 + i * head_step) * sh);
+        fetch_token(A, ring, slot, g, nchunk, lph, in + b * sb + n * sn, sh);
       }
       cp_async_commit();
     };
 #pragma unroll 1
-    for (int s = 0; s < D; ++s) fetch(first + s * step, s, s);
+    for (int s = 0; s < D; ++s) fetch(first + s * step, s * slot_size, s);
     uint64_t w[CPT][4];
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
@@ -219,19 +235,17 @@ __global__ void __launch_bounds__(rope_bounds(CPT)) qkv_rope_kernel(const __grid
       if (norm != VEDA_NORM_NONE && c < nchunk) load_pairs(A.w[which] + (norm == VEDA_NORM_ROW ? 8 * c : ch0), w[i]);
     }
     int slot = 0, aslot = 0;
-    auto next = [](int s, int n) { return s + 1 == n ? 0 : s + 1; };
-    for (int tok = first; tok < A.tokens; tok += step, flip ^= 1, slot = next(slot, D), aslot = next(aslot, D + 2)) {
-      const int b = A.by_n.div(tok), n = tok - b * A.N;
+    auto next = [](int s, int by, int n) { return s + by == n ? 0 : s + by; };
+    for (int tok = first; tok < A.tokens; tok += step, flip ^= 1, slot = next(slot, slot_size, D * slot_size),
+             aslot = next(aslot, 1, D + 2)) {
       uint64_t v[CPT][4];
       cp_async_wait<D - 1>();
+      ring.sync();
 #pragma unroll
       for (int i = 0; i < CPT; ++i) {
-        to_pairs(ring.read(slot, i), v[i]);
-        if (g.t + i * g.tpt >= nchunk) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) v[i][k] = 0;
-        }
+        to_pairs(ring.read(slot, i), v[i]);   // past the row's end: whatever is there
       }
+      ring.sync();
       fetch(tok + D * step, slot, aslot >= 2 ? aslot - 2 : aslot + D);
       if (g.W == 1 || (which < 2 && norm != VEDA_NORM_ROW)) group_sync(g);   // a row's sum is a barrier itself
       if (norm != VEDA_NORM_NONE) {
@@ -242,7 +256,7 @@ __global__ void __launch_bounds__(rope_bounds(CPT)) qkv_rope_kernel(const __grid
           uint64_t s2 = 0;
 #pragma unroll
           for (int k = 0; k < 4; ++k) s2 = f2_fma(v[i][k], v[i][k], s2);
-          r[i] = f2_sum(s2);
+          r[i] = g.t + i * g.tpt < nchunk ? f2_sum(s2) : 0.f;
           ss += r[i];
         }
         if (norm == VEDA_NORM_ROW) {
@@ -255,13 +269,12 @@ __global__ void __launch_bounds__(rope_bounds(CPT)) qkv_rope_kernel(const __grid
         }
 #pragma unroll
         for (int i = 0; i < CPT; ++i) {
-          if (g.t + i * g.tpt < nchunk) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[i][k] = f2_mul(f2_mul(v[i][k], f2_all(r[i])), w[i][k]);
-          }
+          for (int k = 0; k < 4; ++k) v[i][k] = f2_mul(f2_mul(v[i][k], f2_all(r[i])), w[i][k]);
         }
       }
-      const long long row = (long long)b * A.heads * A.N + n;
+      const int b = A.by_n.div(tok), n = tok - b * A.N;
+      __nv_bfloat16* row = out + ((long long)b * A.heads * A.N + n) * A.d;
       float2 cs[Angles<HALVES, D>::kN];
       if (which < 2) angles.read(aslot, ch0, cs);
 #pragma unroll
@@ -269,7 +282,7 @@ __global__ void __launch_bounds__(rope_bounds(CPT)) qkv_rope_kernel(const __grid
         const int head = head0 + i * head_step;
         if (which < 2) angles.apply(v[i], cs, 1.f, scratch, g.lane);
         if (g.t + i * g.tpt < nchunk && VEDA_IN_BOUNDS(head < A.heads && tok < A.tokens))
-          store_pairs(out + (row + (long long)head * A.N) * A.d, v[i]);
+          store_pairs(row + head * A.head_size, v[i]);
       }
     }
   }
@@ -289,13 +302,14 @@ __global__ void __launch_bounds__(512) qkv_rope_bwd_kernel(const __grid_constant
   const int lph = A.d / 8, nchunk = A.heads * lph;
   const int ch0 = (g.t % lph) * 8, head0 = g.t / lph, head_step = g.tpt / lph;
   const int step = gridDim.x * g.groups, first = blockIdx.x * g.groups + g.group;
+  const int slot_size = CPT * blockDim.x;
   const Angles<HALVES, D> angles(A, rest, g, ch0, lph);
   int flip = 0;
   for (int o = 0; o < A.n_order; ++o) {
     if (o > 0) __syncthreads();   // the angles' slots start over
     const int which = A.order[o];
     const int norm = which == 2 ? VEDA_NORM_NONE : A.norm;
-    const T* in = static_cast<const T*>(A.in[which]) + ch0;
+    const T* in = static_cast<const T*>(A.in[which]);
     const long long sb = A.sb[which], sn = A.sn[which], sh = A.sh[which];
     const __nv_bfloat16* dout = static_cast<const __nv_bfloat16*>(A.out[which]) + ch0;
     T* dx = static_cast<T*>(A.dx[which]) + ch0;
@@ -304,20 +318,16 @@ __global__ void __launch_bounds__(512) qkv_rope_bwd_kernel(const __grid_constant
       if (tok < A.tokens) {
         const int b = A.by_n.div(tok), n = tok - b * A.N;
         if (which < 2) angles.fetch(A, g, aslot, n);
-        const long long row = (long long)b * A.heads * A.N + n;
+        const __nv_bfloat16* row = dout + ((long long)b * A.heads * A.N + n) * A.d;
 #pragma unroll
-        for (int i = 0; i < CPT; ++i) {
-          const int head = head0 + i * head_step;
-          if (g.t + i * g.tpt < nchunk) {
-            rg.fetch(slot, i, dout + (row + (long long)head * A.N) * A.d);
-            if (norm != VEDA_NORM_NONE) rx.fetch(slot, i, in + b * sb + n * sn + head * sh);
-          }
-        }
+        for (int i = 0; i < CPT; ++i)
+          if (g.t + i * g.tpt < nchunk) rg.fetch(slot, i, 0, row + (head0 + i * head_step) * A.head_size);
+        if (norm != VEDA_NORM_NONE) fetch_token(A, rx, slot, g, nchunk, lph, in + b * sb + n * sn, sh);
       }
       cp_async_commit();
     };
 #pragma unroll 1
-    for (int s = 0; s < D; ++s) fetch(first + s * step, s, s);
+    for (int s = 0; s < D; ++s) fetch(first + s * step, s * slot_size, s);
     uint64_t w[CPT][4], acc[CPT][4];
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
@@ -327,20 +337,18 @@ __global__ void __launch_bounds__(512) qkv_rope_bwd_kernel(const __grid_constant
       if (norm != VEDA_NORM_NONE && c < nchunk) load_pairs(A.w[which] + (norm == VEDA_NORM_ROW ? 8 * c : ch0), w[i]);
     }
     int slot = 0, aslot = 0;
-    auto next = [](int s, int n) { return s + 1 == n ? 0 : s + 1; };
-    for (int tok = first; tok < A.tokens; tok += step, flip ^= 1, slot = next(slot, D), aslot = next(aslot, D + 2)) {
-      const int b = A.by_n.div(tok), n = tok - b * A.N;
+    auto next = [](int s, int by, int n) { return s + by == n ? 0 : s + by; };
+    for (int tok = first; tok < A.tokens; tok += step, flip ^= 1, slot = next(slot, slot_size, D * slot_size),
+             aslot = next(aslot, 1, D + 2)) {
       uint64_t gv[CPT][4], v[CPT][4];
       cp_async_wait<D - 1>();
+      rx.sync();
 #pragma unroll
       for (int i = 0; i < CPT; ++i) {
         to_pairs(rg.read(slot, i), gv[i]);
         if (norm != VEDA_NORM_NONE) to_pairs(rx.read(slot, i), v[i]);
-        if (g.t + i * g.tpt >= nchunk) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) gv[i][k] = v[i][k] = 0;
-        }
       }
+      rx.sync();
       fetch(tok + D * step, slot, aslot >= 2 ? aslot - 2 : aslot + D);
       if (which < 2) {
         group_sync(g);
@@ -359,8 +367,9 @@ __global__ void __launch_bounds__(512) qkv_rope_bwd_kernel(const __grid_constant
             p1 = f2_fma(v[i][k], v[i][k], p1);
             p2 = f2_fma(f2_mul(gv[i][k], w[i][k]), v[i][k], p2);
           }
-          s1[i] = f2_sum(p1);
-          s2[i] = f2_sum(p2);
+          const bool in = g.t + i * g.tpt < nchunk;   // past the row's end the ring holds anything
+          s1[i] = in ? f2_sum(p1) : 0.f;
+          s2[i] = in ? f2_sum(p2) : 0.f;
         }
         if (norm == VEDA_NORM_ROW) {
           float a = 0.f, c = 0.f;
@@ -377,6 +386,7 @@ __global__ void __launch_bounds__(512) qkv_rope_bwd_kernel(const __grid_constant
         for (int i = 0; i < CPT; ++i) {
           const float rstd = rsqrtf(s1[i] * A.inv_n + A.eps);
           const uint64_t rr = f2_all(rstd), cc = f2_all(-s2[i] * A.inv_n * rstd * rstd);
+          if (g.t + i * g.tpt >= nchunk) continue;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             acc[i][k] = f2_fma(f2_mul(gv[i][k], rr), v[i][k], acc[i][k]);
@@ -384,11 +394,13 @@ __global__ void __launch_bounds__(512) qkv_rope_bwd_kernel(const __grid_constant
           }
         }
       }
+      const int b = A.by_n.div(tok);
+      T* row = dx + b * dsb + (tok - b * A.N) * dsn;
 #pragma unroll
       for (int i = 0; i < CPT; ++i) {
         const int head = head0 + i * head_step;
         if (g.t + i * g.tpt < nchunk && VEDA_IN_BOUNDS(head < A.heads && tok < A.tokens))
-          store_pairs(dx + b * dsb + n * dsn + head * dsh, gv[i]);
+          store_pairs(row + head * dsh, gv[i]);
       }
     }
     float* part = A.part[which];
@@ -405,7 +417,7 @@ __global__ void __launch_bounds__(512) qkv_rope_bwd_kernel(const __grid_constant
 #pragma unroll
       for (int i = 0; i < CPT; ++i) {
         const int c = g.t + i * g.tpt;
-        if (c < nchunk) store_pairs(sums + g.group * C + 8 * c, acc[i]);
+        if (c < nchunk) store_shared(sums + g.group * C + 8 * c, acc[i]);
       }
     } else {
 #pragma unroll
@@ -413,7 +425,7 @@ __global__ void __launch_bounds__(512) qkv_rope_bwd_kernel(const __grid_constant
 #pragma unroll
         for (int k = 0; k < 4; ++k) acc[0][k] = f2_add(acc[0][k], acc[i][k]);
       }
-      store_pairs(sums + (threadIdx.x / lph) * C + ch0, acc[0]);
+      store_shared(sums + (threadIdx.x / lph) * C + ch0, acc[0]);
     }
     __syncthreads();
     for (int c = threadIdx.x; c < C; c += blockDim.x) {
@@ -482,9 +494,10 @@ cudaError_t rope_run(const RopeArgs& a, const RowSplit& r, bool backward, int sm
 }  // namespace
 
 cudaError_t launch_qkv_rope(RopeArgs a, int type, bool backward, int sms, cudaStream_t s) {
-  const RowSplit r = row_split(a.heads * a.d / 8, a.tokens, sms);
+  const RowSplit r = row_split(a.heads * a.d / 8, a.tokens, sms, backward ? 1024 : 256);
   a.warps = r.W;
   a.HW = a.H * a.W;
+  a.head_size = (long long)a.N * a.d;
   a.by_n = FastDiv(a.N);
   a.by_hw = FastDiv(a.HW);
   a.by_w = FastDiv(a.W);

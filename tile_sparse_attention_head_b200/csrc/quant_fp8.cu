@@ -50,8 +50,9 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const __grid_constant__
 #pragma unroll
     for (int off = 8; off; off >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, off));
     if (here && VEDA_IN_BOUNDS(row < A.rows && c + 8 <= A.C)) {
-      *reinterpret_cast<uint2*>(A.q + (long long)row * A.C + c) = to_e4m3(v, kE4M3Max / a);
-      if (l == 0) A.scale[kb * A.rows + row] = a / kE4M3Max;
+      const float s = e4m3_scale(a);
+      *reinterpret_cast<uint2*>(A.q + (long long)row * A.C + c) = to_e4m3(v, reciprocal(s));
+      if (l == 0) A.scale[kb * A.rows + row] = s;
     }
   }
 }
@@ -79,14 +80,14 @@ __global__ void __launch_bounds__(256) quant_weight_kernel(const T* __restrict__
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < 8; ++k) a = max_nan(a, red[k]);
-  const float r = kE4M3Max / a;
+  const float s = e4m3_scale(a), r = reciprocal(s);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int n = n0 + 16 * i;
     if (n < N && c < K && VEDA_IN_BOUNDS(c + 8 <= K))
       *reinterpret_cast<uint2*>(q + (long long)n * K + c) = to_e4m3(v[i], r);
   }
-  if (threadIdx.x == 0) scale[blockIdx.x] = a / kE4M3Max;
+  if (threadIdx.x == 0) scale[blockIdx.x] = s;
 }
 
 cudaError_t launch_quant_rows(QuantArgs a, int type, cudaStream_t s) {

@@ -39,10 +39,10 @@ __global__ void __launch_bounds__(512) add_rms_norm_kernel(const __grid_constant
   const RowGroup g(A.warps);
   const Ring<TX, CPT> rx(ring_raw);
   const Ring<TD, CPT> rd(ring_raw + D * Ring<TX, CPT>::kBytes / 16 * blockDim.x);
-  const int nchunk = A.C / 8;
-  const TX* x = static_cast<const TX*>(A.x) + 8 * g.t;
-  const TD* delta = A.delta == nullptr ? nullptr : static_cast<const TD*>(A.delta) + 8 * g.t;
-  TX* h = static_cast<TX*>(A.h);
+  const int nchunk = A.C / 8, slot_size = CPT * blockDim.x;
+  const RowPieces<TX, CPT> px(g.t, g.tpt, nchunk);
+  const RowPieces<TD, CPT> pd(g.t, g.tpt, nchunk);
+  const bool has_delta = A.delta != nullptr, has_h = A.h != nullptr;
   uint64_t w[CPT][4];
 #pragma unroll
   for (int i = 0; i < CPT; ++i) {
@@ -51,38 +51,43 @@ __global__ void __launch_bounds__(512) add_rms_norm_kernel(const __grid_constant
   }
   const float inv_c = 1.f / (float)A.C;
   const long long step = (long long)gridDim.x * g.groups;
-  auto fetch = [&](long long row, int slot) {
-    if (row < A.rows) {
-#pragma unroll
-      for (int i = 0; i < CPT; ++i) {
-        if (g.t + i * g.tpt < nchunk) {
-          rx.fetch(slot, i, x + row * A.ldx + 8 * i * g.tpt);
-          if (delta != nullptr) rd.fetch(slot, i, delta + row * A.ldd + 8 * i * g.tpt);
-        }
-      }
+  long long row = (long long)blockIdx.x * g.groups + g.group;
+  const TX* x = static_cast<const TX*>(A.x) + row * A.ldx;              // D rows ahead
+  const TD* delta = static_cast<const TD*>(A.delta) + row * A.ldd;
+  TX* h = static_cast<TX*>(A.h) + row * A.C + 8 * g.t;
+  using TY = typename std::conditional<FP8, uint8_t, TD>::type;
+  TY* y = static_cast<TY*>(A.y) + row * A.C + 8 * g.t;
+  float* scale = A.scale + (g.t >> 4) * A.rows;
+  auto fetch = [&](long long r, int slot) {
+    if (r < A.rows) {
+      px.fetch(rx, slot, x);
+      if (has_delta) pd.fetch(rd, slot, delta);
     }
     cp_async_commit();
+    x += step * A.ldx;
+    delta += step * A.ldd;
   };
-  long long row = (long long)blockIdx.x * g.groups + g.group;
 #pragma unroll 1
-  for (int s = 0; s < D; ++s) fetch(row + s * step, s);
-  for (int turn = 0, slot = 0; row < A.rows; row += step, turn ^= 1, slot = slot + 1 == D ? 0 : slot + 1) {
+  for (int s = 0; s < D; ++s) fetch(row + s * step, s * slot_size);
+  for (int turn = 0, slot = 0; row < A.rows; row += step, turn ^= 1) {
     Words<TX> hw[CPT];
     cp_async_wait<D - 1>();
+    rx.sync();
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
       hw[i] = rx.read(slot, i);
-      if (delta != nullptr) add_to(hw[i], rd.read(slot, i));
+      if (has_delta) add_to(hw[i], rd.read(slot, i));
     }
+    rx.sync();
     fetch(row + D * step, slot);
+    slot = slot + slot_size == D * slot_size ? 0 : slot + slot_size;
     uint64_t v[CPT][4];
     uint64_t ss = 0;
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
-      const int c = g.t + i * g.tpt;
       to_pairs(hw[i], v[i]);
-      if (c < nchunk) {
-        if (h != nullptr && VEDA_IN_BOUNDS(row < A.rows)) store_words(h + row * A.C + 8 * c, hw[i]);
+      if (g.t + i * g.tpt < nchunk) {
+        if (has_h && VEDA_IN_BOUNDS(row < A.rows)) store_words(h + 8 * i * g.tpt, hw[i]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) ss = f2_fma(v[i][k], v[i][k], ss);
       }
@@ -92,23 +97,26 @@ __global__ void __launch_bounds__(512) add_rms_norm_kernel(const __grid_constant
     const uint64_t rr = f2_all(rstd);
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
-      const int c = g.t + i * g.tpt;
+      const bool in = g.t + i * g.tpt < nchunk;
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[i][k] = f2_mul(f2_mul(v[i][k], rr), w[i][k]);
       if constexpr (FP8) {
         // Chunks c .. c+15 of an aligned half-warp are one block of 128 channels.
         float a = kTiny;
-        if (c < nchunk) a = max_abs(a, v[i]);
+        if (in) a = max_abs(a, v[i]);
 #pragma unroll
         for (int off = 8; off; off >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, off));
-        if (c < nchunk) {
-          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(A.y) + row * A.C + 8 * c) = to_e4m3(v[i], kE4M3Max / a);
-          if ((c & 15) == 0) A.scale[(long long)(c >> 4) * A.rows + row] = a / kE4M3Max;
+        const float s = e4m3_scale(a);
+        if (in) {
+          *reinterpret_cast<uint2*>(y + 8 * i * g.tpt) = to_e4m3(v[i], reciprocal(s));
+          if ((g.lane & 15) == 0) scale[2 * g.W * i * A.rows + row] = s;
         }
       } else {
-        if (c < nchunk) store_pairs(static_cast<TD*>(A.y) + row * A.C + 8 * c, v[i]);
+        if (in) store_pairs(y + 8 * i * g.tpt, v[i]);
       }
     }
+    h += step * A.C;
+    y += step * A.C;
   }
 }
 
@@ -120,10 +128,10 @@ __global__ void __launch_bounds__(512) add_rms_norm_bwd_kernel(const __grid_cons
   const RowGroup g(A.warps);
   const Ring<TX, CPT> rh(ring_raw), rdh(ring_raw + D * Ring<TX, CPT>::kBytes / 16 * blockDim.x);
   const Ring<TD, CPT> rdy(ring_raw + 2 * D * Ring<TX, CPT>::kBytes / 16 * blockDim.x);
-  const int nchunk = A.C / 8;
-  const TX* h = static_cast<const TX*>(A.h) + 8 * g.t;
-  const TX* dh = A.dh == nullptr ? nullptr : static_cast<const TX*>(A.dh) + 8 * g.t;
-  const TD* dy = static_cast<const TD*>(A.dy) + 8 * g.t;
+  const int nchunk = A.C / 8, slot_size = CPT * blockDim.x;
+  const RowPieces<TX, CPT> px(g.t, g.tpt, nchunk);
+  const RowPieces<TD, CPT> pd(g.t, g.tpt, nchunk);
+  const bool has_dh = A.dh != nullptr, has_dx = A.dx != nullptr, has_dd = A.ddelta != nullptr;
   uint64_t w[CPT][4], acc[CPT][4];
 #pragma unroll
   for (int i = 0; i < CPT; ++i) {
@@ -134,36 +142,35 @@ __global__ void __launch_bounds__(512) add_rms_norm_bwd_kernel(const __grid_cons
   }
   const float inv_c = 1.f / (float)A.C;
   const long long step = (long long)gridDim.x * g.groups;
-  auto fetch = [&](long long row, int slot) {
-    if (row < A.rows) {
-#pragma unroll
-      for (int i = 0; i < CPT; ++i) {
-        const long long at = row * A.C + 8 * i * g.tpt;
-        if (g.t + i * g.tpt < nchunk) {
-          rh.fetch(slot, i, h + at);
-          rdy.fetch(slot, i, dy + at);
-          if (dh != nullptr) rdh.fetch(slot, i, dh + at);
-        }
-      }
+  long long row = (long long)blockIdx.x * g.groups + g.group;
+  long long ahead = row * A.C, here = ahead + 8 * g.t;   // elements: D rows ahead, this row's chunk 0
+  auto fetch = [&](long long r, int slot) {
+    if (r < A.rows) {
+      px.fetch(rh, slot, static_cast<const TX*>(A.h) + ahead);
+      pd.fetch(rdy, slot, static_cast<const TD*>(A.dy) + ahead);
+      if (has_dh) px.fetch(rdh, slot, static_cast<const TX*>(A.dh) + ahead);
     }
     cp_async_commit();
+    ahead += step * A.C;
   };
-  long long row = (long long)blockIdx.x * g.groups + g.group;
 #pragma unroll 1
-  for (int s = 0; s < D; ++s) fetch(row + s * step, s);
+  for (int s = 0; s < D; ++s) fetch(row + s * step, s * slot_size);
   float nrstd = row < A.rows ? A.rstd[row] : 0.f;
-  for (int turn = 0, slot = 0; row < A.rows; row += step, turn ^= 1, slot = slot + 1 == D ? 0 : slot + 1) {
+  for (int turn = 0, slot = 0; row < A.rows; row += step, turn ^= 1) {
     uint64_t hv[CPT][4], gv[CPT][4];
     Words<TX> dv[CPT];
     const float rstd = nrstd;
     cp_async_wait<D - 1>();
+    rh.sync();
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
       to_pairs(rh.read(slot, i), hv[i]);
       to_pairs(rdy.read(slot, i), gv[i]);
-      if (dh != nullptr) dv[i] = rdh.read(slot, i);
+      if (has_dh) dv[i] = rdh.read(slot, i);
     }
+    rh.sync();
     fetch(row + D * step, slot);
+    slot = slot + slot_size == D * slot_size ? 0 : slot + slot_size;
     if (row + step < A.rows) nrstd = A.rstd[row + step];
     const uint64_t rr = f2_all(rstd);
     uint64_t ss = 0;
@@ -182,18 +189,18 @@ __global__ void __launch_bounds__(512) add_rms_norm_bwd_kernel(const __grid_cons
     const uint64_t cc = f2_all(c1);
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
-      const int c = g.t + i * g.tpt;
-      if (c < nchunk) {
+      if (g.t + i * g.tpt < nchunk) {
         uint64_t d[4] = {0, 0, 0, 0};
-        if (dh != nullptr) to_pairs(dv[i], d);
+        if (has_dh) to_pairs(dv[i], d);
 #pragma unroll
         for (int k = 0; k < 4; ++k) d[k] = f2_fma(rr, f2_fma(hv[i][k], cc, gv[i][k]), d[k]);
         if (VEDA_IN_BOUNDS(row < A.rows)) {
-          if (A.dx != nullptr) store_pairs(static_cast<TX*>(A.dx) + row * A.C + 8 * c, d);
-          if (A.ddelta != nullptr) store_pairs(static_cast<TD*>(A.ddelta) + row * A.C + 8 * c, d);
+          if (has_dx) store_pairs(static_cast<TX*>(A.dx) + here + 8 * i * g.tpt, d);
+          if (has_dd) store_pairs(static_cast<TD*>(A.ddelta) + here + 8 * i * g.tpt, d);
         }
       }
     }
+    here += step * A.C;
   }
   if (A.part == nullptr) return;
   cp_async_wait<0>();
@@ -202,7 +209,7 @@ __global__ void __launch_bounds__(512) add_rms_norm_bwd_kernel(const __grid_cons
 #pragma unroll
   for (int i = 0; i < CPT; ++i) {
     const int c = g.t + i * g.tpt;
-    if (c < nchunk) store_pairs(sums + g.group * A.C + 8 * c, acc[i]);
+    if (c < nchunk) store_shared(sums + g.group * A.C + 8 * c, acc[i]);
   }
   __syncthreads();
   for (int c = threadIdx.x; c < A.C; c += blockDim.x) {
