@@ -243,9 +243,8 @@ cudaError_t launch_rope_table(int n, int dim, double theta, double start, double
 cudaError_t launch_quant_rows(QuantArgs a, int type, cudaStream_t s);
 cudaError_t launch_quant_weight(const void* w, int type, int N, int K, uint8_t* q, float* scale, cudaStream_t s);
 
-void gemm_fp8_boxes(const GemmArgs& a, int* rows_a, int* rows_b);
-cudaError_t launch_gemm_fp8(const CUtensorMap& ta, const CUtensorMap& tb, const GemmArgs& a, int out_type, int sms,
-                            cudaStream_t s);
+cudaError_t launch_gemm_fp8(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc, const GemmArgs& a,
+                            int out_type, int sms, cudaStream_t s);
 
 cudaError_t launch_timeout_selftest(uint64_t timeout_ns, cudaStream_t s);
 cudaError_t launch_bounds_selftest(cudaStream_t s);

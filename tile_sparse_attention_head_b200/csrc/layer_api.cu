@@ -112,19 +112,21 @@ size_t rope_part_bytes(const RopeArgs& a) {
   return round256(sizeof(float) * C * qkv_rope_bwd_parts(a.tokens, a.heads, a.d, sm_count()));
 }
 
-// 2D view [rows, K] of an e4m3 operand, boxes of 128 channels x box_rows rows,
-// 128-byte swizzle; channels and rows past the end read as zero.
-veda_status encode_e4m3(const void* ptr, int64_t ld, int rows, int K, int box_rows, CUtensorMap* out) {
+// 2D view [rows, cols] with a row stride of ld elements, boxes of box_rows rows x
+// 128 bytes, 128-byte swizzle; reads past the end give zero, writes there are
+// dropped.
+veda_status encode_rows(CUtensorMapDataType type, int size, const void* ptr, int64_t ld, int rows, int cols,
+                        int box_rows, CUtensorMap* out) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return fail(VEDA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)ld};
-  const cuuint32_t box[2] = {128u, (cuuint32_t)box_rows};
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld * size};
+  const cuuint32_t box[2] = {128u / size, (cuuint32_t)box_rows};
   const cuuint32_t estr[2] = {1u, 1u};
-  const CUresult r = fn(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const CUresult r = fn(out, type, 2, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(VEDA_ERR_CUDA, "cuTensorMapEncodeTiled (e4m3 operand) failed (CUresult %d)", (int)r);
+  if (r != CUDA_SUCCESS) return fail(VEDA_ERR_CUDA, "cuTensorMapEncodeTiled (matrix) failed (CUresult %d)", (int)r);
   return VEDA_OK;
 }
 
@@ -250,7 +252,7 @@ veda_status veda_gemm_fp8(int32_t M, int32_t N, int32_t K, const void* a, int64_
   if (M > (1 << 30) || N > (1 << 30) || K > (1 << 30)) return fail(VEDA_ERR_UNSUPPORTED, "M, N and K must be at most 2^30");
   if (lda < K || lda % 16 || ldb < K || ldb % 16 || lda > (1LL << 39) || ldb > (1LL << 39))
     return fail(VEDA_ERR_INVALID_ARG, "lda and ldb must be multiples of 16 of at least K");
-  if (ldo < N || ldo % 8) return fail(VEDA_ERR_INVALID_ARG, "ldo must be a multiple of 8 of at least N");
+  if (ldo < N || ldo % 8 || ldo > (1LL << 37)) return fail(VEDA_ERR_INVALID_ARG, "ldo must be a multiple of 8 of at least N");
   if (out_type != VEDA_BF16 && out_type != VEDA_FP32) return fail(VEDA_ERR_UNSUPPORTED, "out must be bf16 or fp32");
   if (M == 0) return ok();
   if (!a || !a_scale || !b || !b_scale || !out) return fail(VEDA_ERR_INVALID_ARG, "NULL tensor argument");
@@ -272,13 +274,15 @@ veda_status veda_gemm_fp8(int32_t M, int32_t N, int32_t K, const void* a, int64_
   g.out = out;
   g.ldo = ldo;
   g.timeout_ns = g_timeout_ns;
-  int rows_a = 0, rows_b = 0;
-  gemm_fp8_boxes(g, &rows_a, &rows_b);
-  CUtensorMap ta, tb;
+  CUtensorMap ta, tb, tc;
   veda_status s;
-  if ((s = encode_e4m3(a, lda, M, K, rows_a, &ta)) != VEDA_OK || (s = encode_e4m3(b, ldb, N, K, rows_b, &tb)) != VEDA_OK)
+  const bool wide = out_type == VEDA_FP32;
+  if ((s = encode_rows(CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a, lda, M, K, 128, &ta)) != VEDA_OK ||
+      (s = encode_rows(CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, b, ldb, N, K, 128, &tb)) != VEDA_OK ||
+      (s = encode_rows(wide ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, wide ? 4 : 2, out, ldo,
+                       M, N, 32, &tc)) != VEDA_OK)
     return s;
-  const cudaError_t e = launch_gemm_fp8(ta, tb, g, out_type, sm_count(), (cudaStream_t)stream);
+  const cudaError_t e = launch_gemm_fp8(ta, tb, tc, g, out_type, sm_count(), (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "veda_gemm_fp8");
   return ok();
 }
