@@ -229,6 +229,7 @@ struct GemmArgs {
   long long ldo;
   uint64_t timeout_ns;
   int tiles_m, tiles_n, tiles;
+  int few, split;               // rows per tile of the kernel for few rows (0: the other one), CTAs per tile
 };
 
 cudaError_t launch_add_rms_norm(NormArgs a, int tx, int td, bool fp8, int sms, cudaStream_t s);
@@ -243,6 +244,7 @@ cudaError_t launch_rope_table(int n, int dim, double theta, double start, double
 cudaError_t launch_quant_rows(QuantArgs a, int type, cudaStream_t s);
 cudaError_t launch_quant_weight(const void* w, int type, int N, int K, uint8_t* q, float* scale, cudaStream_t s);
 
+void plan_gemm_fp8(GemmArgs* a, int sms);
 cudaError_t launch_gemm_fp8(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc, const GemmArgs& a,
                             int out_type, int sms, cudaStream_t s);
 
