@@ -679,6 +679,20 @@ def veda_qkv_norm_rope(r: veda_rope, q: Optional[torch.Tensor], k: Optional[torc
           _at(k_out, "k_out", dev, torch.bfloat16, outs), _at(v_out, "v_out", dev, torch.bfloat16, outs))
 
 
+def _packed_norm_rope(r: veda_rope, qkv: torch.Tensor, wq: Optional[torch.Tensor], wk: Optional[torch.Tensor], outs) -> None:
+    """veda_qkv_norm_rope of one packed [B, N, 3, heads, d] tensor of r's sizes into three grid-order tensors that the
+    caller has just made: the operands' checks once instead of three times."""
+    dev, code, e = _device(qkv, "qkv"), _type(qkv, "qkv"), qkv.element_size()
+    sb, sn, s3, sh, sc = qkv.stride()
+    if sc != 1:
+        raise ValueError("the channels of qkv must be contiguous")
+    p, n = qkv.data_ptr(), qkv.shape[1]
+    sb, sn, sh = sb if r.B > 1 else 0, sn if n > 1 else 0, sh if r.heads > 1 else 0
+    q, k, v = (ctypes.byref(veda_tokens(p + i * s3 * e, sb, sn, sh)) for i in range(3))
+    _call("veda_qkv_norm_rope", dev, None, ctypes.byref(r), code, q, k, v, _norm_weight(wq, r, "wq", dev),
+          _norm_weight(wk, r, "wk", dev), outs[0].data_ptr(), outs[1].data_ptr(), outs[2].data_ptr())
+
+
 def veda_qkv_norm_rope_backward_workspace(r: veda_rope, device=None) -> int:
     n = _SZ()
     _on_device(device, lambda: _check(LIB.veda_qkv_norm_rope_backward_workspace(ctypes.byref(r), ctypes.byref(n)),

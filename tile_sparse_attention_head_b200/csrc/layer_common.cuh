@@ -231,15 +231,15 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 // How rows are spread over threads: a row belongs to `W` warps of a CTA (its
 // group), `cpt` chunks per thread, and a CTA has up to as many groups as make
-// 16 warps.  Thread t of a group has the chunks t, t + 32 W, ...
+// 16 warps (or what the kernel with two chunks per thread has registers for).  Thread t of a group has the chunks t, t + 32 W, ...
 struct RowSplit {
   int cpt, W, groups, threads;
 };
-inline RowSplit row_split(int nchunk, long long rows, int sms, int most_for_two = 1024) {
+inline RowSplit row_split(int nchunk, long long rows, int sms, int most_for_two = 1024, int warps_for_two = 16) {
   RowSplit r;
   r.cpt = nchunk <= 32 ? 1 : nchunk <= most_for_two ? 2 : 4;
   r.W = (nchunk + 32 * r.cpt - 1) / (32 * r.cpt);
-  r.groups = 16 / r.W;
+  r.groups = (r.cpt == 2 ? warps_for_two : 16) / r.W;
   const long long each = (rows + sms - 1) / sms;   // few rows: spread them over the SMs first
   if (each < r.groups) r.groups = each < 1 ? 1 : (int)each;
   r.threads = 32 * r.W * r.groups;

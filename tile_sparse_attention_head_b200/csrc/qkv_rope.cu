@@ -494,7 +494,8 @@ cudaError_t rope_run(const RopeArgs& a, const RowSplit& r, bool backward, int sm
 }  // namespace
 
 cudaError_t launch_qkv_rope(RopeArgs a, int type, bool backward, int sms, cudaStream_t s) {
-  const RowSplit r = row_split(a.heads * a.d / 8, a.tokens, sms, backward ? 1024 : 256);
+  const RowSplit r = backward ? row_split(a.heads * a.d / 8, a.tokens, sms)
+                              : row_split(a.heads * a.d / 8, a.tokens, sms, 256, 20);
   a.warps = r.W;
   a.HW = a.H * a.W;
   a.head_size = (long long)a.N * a.d;

@@ -143,7 +143,7 @@ def add_rms_norm_fp8(x: torch.Tensor, delta: Optional[torch.Tensor], weight: tor
     x2, d2 = _flat(x), _flat(delta)
     rows, C = x2.shape
     h = torch.empty_like(x2) if delta is not None else None
-    y8 = x2.new_empty((rows, C), dtype=B.FP8)
+    y8 = torch.empty_like(x2, dtype=B.FP8)
     scale = x2.new_empty(((C + 127) // 128, rows), dtype=torch.float32)
     B.veda_add_rms_norm_fp8(x2, d2, weight, eps, h, y8, scale)
     return x if h is None else h if x.dim() == 2 else h.view(x.shape), y8, scale
@@ -278,7 +278,6 @@ def qkv_norm_rope(qkv, grid: Sequence[int], tables: Sequence[Optional[torch.Tens
         if len(xs) != 3 or any(t.dim() != 4 for t in xs):
             raise ValueError("qkv must be a packed tensor or (q, k, v), each [B, N, heads, d]")
         b, n, heads, d = xs[0].shape
-    grid = tuple(int(g) for g in grid)
     if len(grid) != 3 or n != grid[0] * grid[1] * grid[2]:
         raise ValueError(f"N = {n} tokens do not fill the grid {grid}")
     if norm != "none" and (wq is None or wk is None):
@@ -291,9 +290,12 @@ def qkv_norm_rope(qkv, grid: Sequence[int], tables: Sequence[Optional[torch.Tens
     rope = B.make_rope(b, heads, d, grid, tables, pairing, norm, eps)
     if _wants_grad(wq, wk, *xs):
         return _QkvNormRope.apply(rope, tuple(tables), wq, wk, *xs)
-    q, k, v = xs[0].unbind(2) if len(xs) == 1 else xs
-    outs = tuple(q.new_empty((b, heads, n, d), dtype=torch.bfloat16) for _ in range(3))
-    B.veda_qkv_norm_rope(rope, q, k, v, wq, wk, *outs)
+    if len(xs) == 1:      # one allocation: with three a call on one token is a tenth slower
+        outs = qkv.new_empty((3, b, heads, n, d), dtype=torch.bfloat16).unbind(0)
+        B._packed_norm_rope(rope, qkv, wq, wk, outs)
+    else:
+        outs = tuple(xs[0].new_empty((b, heads, n, d), dtype=torch.bfloat16) for _ in range(3))
+        B.veda_qkv_norm_rope(rope, *xs, wq, wk, *outs)
     return outs
 
 
