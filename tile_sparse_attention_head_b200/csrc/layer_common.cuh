@@ -308,11 +308,13 @@ inline unsigned resident_ctas(K kernel, int threads, size_t smem, int sms) {
 
 // The 8-bit rule: a block's scale is s = a / 448 with a its largest magnitude,
 // but at least 2^-100 (so that a block of zeros has a scale and 1 / s stays
-// finite), and the block holds e4m3(x / s), nearest even.  Both quotients are
-// products with a reciprocal, to fp32's last places: a division's full
-// sequence, twice per 8 channels, was a fifth of the instructions.  The maximum
+// finite), and the block holds e4m3(x / s), nearest even.  The scale is a
+// product with 1 / 448; the norm multiplies by an approximate reciprocal of it
+// (full divisions, twice per 8 channels, were a fifth of its instructions), the
+// quantisers by 448 / a.  The maximum
 // passes NaN on: a block with an infinity or NaN gets a scale that is infinite
 // or NaN, and stands for NaN as a whole, rather than for a finite wrong value.
+constexpr float kE4M3Max = 448.f;
 constexpr float kTiny = 7.888609052210118e-31f;   // 2^-100
 
 __device__ __forceinline__ float e4m3_scale(float a) { return a * (1.f / 448.f); }
