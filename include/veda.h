@@ -364,12 +364,11 @@ typedef enum { VEDA_BF16 = 0, VEDA_FP16 = 1, VEDA_FP32 = 2 } veda_dtype;
  * stream's; delta [rows, C] (row stride ldd) and y of delta_type, the
  * sublayers'.  The two types are equal, or VEDA_FP32 and VEDA_BF16.  delta may
  * be NULL (then h = x); h may be NULL, and may be x itself if ldx == C.
- * weight [C] fp32.  rstd [rows] fp32 or NULL: the factor above, for the backward
- * call.  h and y are dense [rows, C].  C a multiple of 8 in [8, 16384]; ldx and
- * ldd multiples of 8, at least C; rows >= 0; eps >= 0. */
+ * weight [C] fp32.  h and y are dense [rows, C].  C a multiple of 8 in [8, 16384];
+ * ldx and ldd multiples of 8, at least C; rows >= 0; eps >= 0. */
 veda_status veda_add_rms_norm(int64_t rows, int32_t C, veda_dtype x_type, const void* x, int64_t ldx,
                               veda_dtype delta_type, const void* delta, int64_t ldd, const float* weight, float eps,
-                              void* h, void* y, float* rstd, void* stream);
+                              void* h, void* y, void* stream);
 
 /* The same with y in 8 bits: y8 [rows, C] e4m3, y_scale [ceil(C/128), rows]
  * fp32.  Per row and block of 128 channels, with a the block's largest |y| or
@@ -385,7 +384,7 @@ veda_status veda_add_rms_norm_fp8(int64_t rows, int32_t C, veda_dtype x_type, co
  * device: it depends on the number of SMs). */
 veda_status veda_add_rms_norm_backward_workspace(int64_t rows, int32_t C, size_t* bytes);
 
-/* Gradients of veda_add_rms_norm.  h and rstd as the forward wrote them; dy
+/* Gradients of veda_add_rms_norm.  h as the forward wrote it, eps as given to it; dy
  * [rows, C] of delta_type and dh [rows, C] of x_type (or NULL: zero), the
  * upstream gradients of y and of h.  With g = dy * weight:
  *   d = dh + rstd (g - h mean_c(g h) rstd^2),   dweight = sum_rows dy h rstd.
@@ -397,7 +396,7 @@ veda_status veda_add_rms_norm_backward_workspace(int64_t rows, int32_t C, size_t
  * bits. */
 veda_status veda_add_rms_norm_backward(int64_t rows, int32_t C, veda_dtype x_type, const void* h,
                                        veda_dtype delta_type, const void* dy, const void* dh, const float* weight,
-                                       const float* rstd, void* dx, void* ddelta, float* dweight, void* workspace,
+                                       float eps, void* dx, void* ddelta, float* dweight, void* workspace,
                                        size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------- around the attention: 8-bit product */

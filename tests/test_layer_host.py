@@ -22,10 +22,10 @@ BF16, FP16, FP32 = 0, 1, 2
 INVALID, UNSUPPORTED = 1, 2
 
 
-def norm_args(**kw):
+def norm_args(scale=True, **kw):
     a = dict(rows=4, C=64, xt=BF16, x=PTR, ldx=64, dt=BF16, delta=PTR, ldd=64, w=PTR, eps=1e-6, h=PTR, y=PTR, s=PTR)
     a.update(kw)
-    return list(a.values()) + [None]
+    return [v for k, v in a.items() if scale or k != "s"] + [None]
 
 
 @pytest.mark.parametrize("bad", [
@@ -35,7 +35,7 @@ def norm_args(**kw):
     dict(delta=PTR + 2), dict(h=PTR + 4), dict(y=PTR + 4), dict(w=PTR + 4), dict(ldx=72, h=PTR)])
 def test_norm_refusals(V, bad):
     for name in ("veda_add_rms_norm", "veda_add_rms_norm_fp8"):
-        assert getattr(V.LIB, name)(*norm_args(**bad)) != 0, bad
+        assert getattr(V.LIB, name)(*norm_args(name.endswith("fp8"), **bad)) != 0, bad
         assert V.LIB.veda_last_error().decode()
 
 
@@ -44,19 +44,19 @@ def test_norm_fp8_needs_a_scale(V):
 
 
 def test_no_rows_is_no_work(V):
-    assert V.LIB.veda_add_rms_norm(*norm_args(rows=0)) == 0
+    assert V.LIB.veda_add_rms_norm(*norm_args(False, rows=0)) == 0
     assert V.LIB.veda_add_rms_norm_fp8(*norm_args(rows=0)) == 0
-    assert V.LIB.veda_add_rms_norm_backward(0, 64, BF16, PTR, BF16, PTR, None, PTR, PTR, PTR, None, None, None, 0, None) == 0
+    assert V.LIB.veda_add_rms_norm_backward(0, 64, BF16, PTR, BF16, PTR, None, PTR, 1e-6, PTR, None, None, None, 0, None) == 0
     assert V.LIB.veda_quant_fp8(1, 0, 2, 64, BF16, PTR, 0, 64, 64, PTR, PTR, None) == 0
     assert V.LIB.veda_gemm_fp8(0, 64, 64, PTR, 64, PTR, PTR, 64, PTR, None, BF16, PTR, 64, None) == 0
     assert V.LIB.veda_rope_table(0, 32, 1e4, 0.0, 1.0, PTR, None) == 0
 
 
 @pytest.mark.parametrize("bad", [
-    dict(h=None), dict(dy=None), dict(w=None), dict(rstd=None), dict(dx=None, dd=None, dw=None), dict(ws=None),
+    dict(h=None), dict(dy=None), dict(w=None), dict(eps=-1.0), dict(eps=float("nan")), dict(dx=None, dd=None, dw=None), dict(ws=None),
     dict(wsb=0), dict(h=PTR + 8), dict(dw=PTR + 4), dict(ws=PTR + 8), dict(C=12), dict(xt=FP16)])
 def test_norm_backward_refusals(V, bad):
-    a = dict(rows=4, C=64, xt=BF16, h=PTR, dt=BF16, dy=PTR, dh=PTR, w=PTR, rstd=PTR, dx=PTR, dd=PTR, dw=PTR, ws=PTR,
+    a = dict(rows=4, C=64, xt=BF16, h=PTR, dt=BF16, dy=PTR, dh=PTR, w=PTR, eps=1e-6, dx=PTR, dd=PTR, dw=PTR, ws=PTR,
              wsb=16)
     a.update(bad)
     assert V.LIB.veda_add_rms_norm_backward(*a.values(), None) != 0

@@ -99,10 +99,10 @@ _SIG = {
     "veda_attn_backward_workspace": [_P, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)],
     "veda_tile_sparse_attn_backward_grid": [_P, _V, _V, _V, _V, _V, _V, _V, ctypes.c_int32, ctypes.c_float, _V, _V,
                                             _V, _V, ctypes.c_size_t, _V],
-    "veda_add_rms_norm": [_I64, _I32, _I32, _V, _I64, _I32, _V, _I64, _V, _F, _V, _V, _V, _V],
+    "veda_add_rms_norm": [_I64, _I32, _I32, _V, _I64, _I32, _V, _I64, _V, _F, _V, _V, _V],
     "veda_add_rms_norm_fp8": [_I64, _I32, _I32, _V, _I64, _I32, _V, _I64, _V, _F, _V, _V, _V, _V],
     "veda_add_rms_norm_backward_workspace": [_I64, _I32, ctypes.POINTER(_SZ)],
-    "veda_add_rms_norm_backward": [_I64, _I32, _I32, _V, _I32, _V, _V, _V, _V, _V, _V, _V, _V, _SZ, _V],
+    "veda_add_rms_norm_backward": [_I64, _I32, _I32, _V, _I32, _V, _V, _V, _F, _V, _V, _V, _V, _SZ, _V],
     "veda_quant_fp8": [_I32, _I64, _I32, _I32, _I32, _V, _I64, _I64, _I64, _V, _V, _V],
     "veda_quant_fp8_weight": [_I32, _I32, _I32, _V, _V, _V, _V],
     "veda_gemm_fp8": [_I32, _I32, _I32, _V, _I64, _V, _V, _I64, _V, _V, _I32, _V, _I64, _V],
@@ -496,8 +496,7 @@ def _on_device(device, fn):
 
 
 def veda_add_rms_norm(x: torch.Tensor, delta: Optional[torch.Tensor], weight: torch.Tensor, eps: float,
-                      h: Optional[torch.Tensor], y: torch.Tensor, rstd: Optional[torch.Tensor] = None,
-                      stream=None) -> torch.Tensor:
+                      h: Optional[torch.Tensor], y: torch.Tensor, stream=None) -> torch.Tensor:
     """h = x + delta and its RMS norm y, [rows, C]; y is of delta's type (x's without a delta)."""
     dev, shape = _device(x, "x"), x.shape
     xp, ldx = _rows(x, "x", dev)
@@ -505,7 +504,7 @@ def veda_add_rms_norm(x: torch.Tensor, delta: Optional[torch.Tensor], weight: to
     td = y.dtype if delta is None else delta.dtype
     _call("veda_add_rms_norm", dev, stream, shape[0], shape[1], _type(x, "x"), xp, ldx,
           _type(y, "y") if delta is None else _type(delta, "delta"), dp, ldd, _at(weight, "weight", dev, _F32, shape[1:]),
-          eps, _at(h, "h", dev, x.dtype, shape), _at(y, "y", dev, td, shape), _at(rstd, "rstd", dev, _F32, shape[:1]))
+          eps, _at(h, "h", dev, x.dtype, shape), _at(y, "y", dev, td, shape))
     return y
 
 
@@ -525,15 +524,69 @@ def veda_add_rms_norm_fp8(x: torch.Tensor, delta: Optional[torch.Tensor], weight
     return y8
 
 
+# The three below run the same library functions for layer.py, on tensors that
+# it has laid out or made itself (rows, and outputs of the right shape on the
+# right device): only what comes from the caller unseen is checked.
+
+def _layer_norm_forward(x, delta, weight, eps, h, y, scale) -> None:
+    dev = x.get_device()
+    rows, C = x.shape
+    tx = _DTYPES.get(x.dtype)
+    if dev < 0 or tx is None:
+        _device(x, "x"), _type(x, "x")
+    if delta is None:
+        td, dp, ldd = tx, None, 0
+    else:
+        if delta.get_device() != dev:
+            _rows(delta, "delta", dev)
+        td, dp, ldd = _type(delta, "delta"), delta.data_ptr(), delta.stride(0) if rows > 1 else C
+    args = (rows, C, tx, x.data_ptr(), x.stride(0) if rows > 1 else C, td, dp, ldd,
+            _at(weight, "weight", dev, _F32, (C,)), eps, None if h is None else h.data_ptr(), y.data_ptr())
+    if scale is None:
+        _call("veda_add_rms_norm", dev, None, *args)
+    else:
+        _call("veda_add_rms_norm_fp8", dev, None, *args, scale.data_ptr())
+
+
+def _layer_norm_backward(h, dy, dh, weight, eps, dx, ddelta, dweight) -> None:
+    dev = h.get_device()
+    rows, C = h.shape
+    ws, size = None, 0
+    if dweight is not None:
+        size = veda_add_rms_norm_backward_workspace(rows, C, dev)
+        ws = h.new_empty(size, dtype=torch.uint8)
+    _call("veda_add_rms_norm_backward", dev, None, rows, C, _DTYPES[h.dtype], h.data_ptr(), _type(dy, "dy"), dy.data_ptr(),
+          None if dh is None else dh.data_ptr(), weight.data_ptr(), eps,
+          None if dx is None else dx.data_ptr(), None if ddelta is None else ddelta.data_ptr(),
+          None if dweight is None else dweight.data_ptr(), None if ws is None else ws.data_ptr(), size)
+
+
+def _layer_gemm(a, a_scale, b, b_scale, bias, out_dtype) -> torch.Tensor:
+    dev = _device(a, "a")
+    ap, lda = _rows(a, "a", dev)
+    bp, ldb = _rows(b, "b", dev)
+    (M, K), (N, Kb) = a.shape, b.shape
+    if a.dtype is not FP8 or b.dtype is not FP8 or Kb != K:
+        raise ValueError(f"a and b must be {FP8} [M, K] and [N, K] (got {a.dtype} {tuple(a.shape)}, {b.dtype} {tuple(b.shape)})")
+    kb = (K + 127) // 128
+    out = a.new_empty((M, N), dtype=out_dtype)
+    _call("veda_gemm_fp8", dev, None, M, N, K, ap, lda, _at(a_scale, "a_scale", dev, _F32, (kb, M)), bp, ldb,
+          _at(b_scale, "b_scale", dev, _F32, ((N + 127) // 128, kb)), _at(bias, "bias", dev, _F32, (N,)),
+          _type(out, "out"), out.data_ptr(), N)
+    return out
+
+
 def veda_add_rms_norm_backward_workspace(rows: int, C: int, device=None) -> int:
     n = _SZ()
-    _on_device(device, lambda: _check(LIB.veda_add_rms_norm_backward_workspace(rows, C, ctypes.byref(n)),
-                                      "veda_add_rms_norm_backward_workspace"))
+    if device is not None and device != torch._C._cuda_getDevice():
+        with torch.cuda.device(device):
+            return veda_add_rms_norm_backward_workspace(rows, C)
+    _check(LIB.veda_add_rms_norm_backward_workspace(rows, C, ctypes.byref(n)), "veda_add_rms_norm_backward_workspace")
     return n.value
 
 
 def veda_add_rms_norm_backward(h: torch.Tensor, dy: torch.Tensor, dh: Optional[torch.Tensor], weight: torch.Tensor,
-                               rstd: torch.Tensor, dx: Optional[torch.Tensor], ddelta: Optional[torch.Tensor],
+                               eps: float, dx: Optional[torch.Tensor], ddelta: Optional[torch.Tensor],
                                dweight: Optional[torch.Tensor], workspace: Optional[torch.Tensor],
                                stream=None) -> None:
     """Gradients of veda_add_rms_norm: dx in h's type, ddelta in dy's type, dweight fp32; None leaves one out."""
@@ -543,7 +596,7 @@ def veda_add_rms_norm_backward(h: torch.Tensor, dy: torch.Tensor, dh: Optional[t
     th, td = h.dtype, dy.dtype
     _call("veda_add_rms_norm_backward", dev, stream, shape[0], shape[1], _type(h, "h"), _at(h, "h", dev, th, shape),
           _type(dy, "dy"), _at(dy, "dy", dev, td, shape), _at(dh, "dh", dev, th, shape),
-          _at(weight, "weight", dev, _F32, shape[1:]), _at(rstd, "rstd", dev, _F32, shape[:1]),
+          _at(weight, "weight", dev, _F32, shape[1:]), eps,
           _at(dx, "dx", dev, th, shape), _at(ddelta, "ddelta", dev, td, shape),
           _at(dweight, "dweight", dev, _F32, shape[1:]), *_scratch(workspace, dev))
 

@@ -612,13 +612,18 @@ cudaError_t gemm_run(const CUtensorMap& ta, const CUtensorMap& tb, const CUtenso
                      cudaStream_t s) {
   using C = GemmCfg;
   auto kernel = gemm_fp8_kernel<TO>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+  static PerDevice once;
+  static std::atomic<int> regs{0};
+  cudaError_t e = once.allow_smem(kernel, C::kSmem);
   if (e != cudaSuccess) return e;
   // The register split (128 threads at 56, 256 at 224) must fit what the block
   // is launched with, or the raise would wait forever.
-  cudaFuncAttributes attr;
-  if ((e = cudaFuncGetAttributes(&attr, kernel)) != cudaSuccess) return e;
-  if (128 * 56 + 256 * 224 > C::kThreads * attr.numRegs) return cudaErrorInvalidConfiguration;
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes attr;
+    if ((e = cudaFuncGetAttributes(&attr, kernel)) != cudaSuccess) return e;
+    regs.store(attr.numRegs, std::memory_order_relaxed);
+  }
+  if (128 * 56 + 256 * 224 > C::kThreads * regs.load(std::memory_order_relaxed)) return cudaErrorInvalidConfiguration;
   a.tiles_m = (a.M + 255) / 256;
   a.tiles_n = (a.N + 255) / 256;
   a.tiles = a.tiles_m * a.tiles_n;
@@ -630,7 +635,8 @@ template <int TN, typename TO>
 cudaError_t gemm_few_run(const CUtensorMap& tx, const CUtensorMap& tw, GemmArgs a, cudaStream_t s) {
   using C = FewCfg<TN>;
   auto kernel = gemm_few_kernel<TN, TO>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+  static PerDevice once;
+  const cudaError_t e = once.allow_smem(kernel, C::kSmem);
   if (e != cudaSuccess) return e;
   a.tiles_n = a.nblocks;
   a.tiles_m = (a.M + TN - 1) / TN;

@@ -168,7 +168,6 @@ struct NormArgs {
   void* h;             // [rows, C] or null
   void* y;             // [rows, C] in delta's type, or e4m3
   float* scale;        // e4m3 only: [ceil(C/128), rows]
-  float* rstd;         // [rows] or null
   int warps;           // per row
 };
 
@@ -176,7 +175,8 @@ struct NormBwdArgs {
   long long rows;
   int C;
   const void *h, *dy, *dh;
-  const float *w, *rstd;
+  const float* w;
+  float eps;
   void *dx, *ddelta;   // either may be null
   float* part;         // [parts, C] or null
   float* dw;
@@ -238,7 +238,7 @@ cudaError_t launch_add_rms_norm_bwd(NormBwdArgs a, int tx, int td, int sms, cuda
 cudaError_t launch_sum_partials(const SumArgs& a, int n, cudaStream_t s);
 
 cudaError_t launch_qkv_rope(RopeArgs a, int type, bool backward, int sms, cudaStream_t s);
-int qkv_rope_bwd_parts(long long tokens, int heads, int d, int sms);
+int qkv_rope_bwd_parts(long long tokens, int sms);
 cudaError_t launch_rope_table(int n, int dim, double theta, double start, double step, float* out, cudaStream_t s);
 
 cudaError_t launch_quant_rows(QuantArgs a, int type, cudaStream_t s);

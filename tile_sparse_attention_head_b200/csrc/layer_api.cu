@@ -18,7 +18,7 @@ veda_status check_norm(int64_t rows, int32_t C, int x_type, int delta_type) {
 
 veda_status norm_forward(const char* name, bool fp8, int64_t rows, int32_t C, int x_type, const void* x, int64_t ldx,
                          int delta_type, const void* delta, int64_t ldd, const float* weight, float eps, void* h,
-                         void* y, float* scale, float* rstd, void* stream) {
+                         void* y, float* scale, void* stream) {
   veda_status s = check_norm(rows, C, x_type, delta_type);
   if (s != VEDA_OK) return s;
   if (!(eps >= 0.f) || std::isinf(eps)) return fail(VEDA_ERR_INVALID_ARG, "eps must be finite and >= 0");
@@ -27,7 +27,7 @@ veda_status norm_forward(const char* name, bool fp8, int64_t rows, int32_t C, in
   if (rows == 0) return ok();
   if (!x || !weight || !y || (fp8 && !scale)) return fail(VEDA_ERR_INVALID_ARG, "NULL tensor argument");
   if (h == x && ldx != C) return fail(VEDA_ERR_INVALID_ARG, "h may be x only if x is dense");
-  const void* ptrs[] = {x, delta, weight, h, y, scale, rstd};
+  const void* ptrs[] = {x, delta, weight, h, y, scale};
   for (const void* p : ptrs)
     if (!aligned16(p)) return fail(VEDA_ERR_INVALID_ARG, "tensor arguments must be 16-byte aligned");
   NormArgs a;
@@ -43,7 +43,6 @@ veda_status norm_forward(const char* name, bool fp8, int64_t rows, int32_t C, in
   a.h = h;
   a.y = y;
   a.scale = scale;
-  a.rstd = rstd;
   const cudaError_t e = launch_add_rms_norm(a, x_type, delta_type, fp8, sm_count(), (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, name);
   return ok();
@@ -109,7 +108,7 @@ size_t rope_part_bytes(const RopeArgs& a) {
   if (a.norm == VEDA_NORM_NONE) return 0;
   const bool row = a.norm == VEDA_NORM_ROW;
   const size_t C = row ? (size_t)a.heads * a.d : (size_t)a.d;
-  return round256(sizeof(float) * C * qkv_rope_bwd_parts(a.tokens, a.heads, a.d, sm_count()));
+  return round256(sizeof(float) * C * qkv_rope_bwd_parts(a.tokens, sm_count()));
 }
 
 // 2D view [rows, cols] with a row stride of ld elements, boxes of box_rows rows x
@@ -137,16 +136,16 @@ extern "C" {
 
 veda_status veda_add_rms_norm(int64_t rows, int32_t C, veda_dtype x_type, const void* x, int64_t ldx,
                               veda_dtype delta_type, const void* delta, int64_t ldd, const float* weight, float eps,
-                              void* h, void* y, float* rstd, void* stream) {
+                              void* h, void* y, void* stream) {
   return norm_forward("veda_add_rms_norm", false, rows, C, x_type, x, ldx, delta_type, delta, ldd, weight, eps, h, y,
-                      nullptr, rstd, stream);
+                      nullptr, stream);
 }
 
 veda_status veda_add_rms_norm_fp8(int64_t rows, int32_t C, veda_dtype x_type, const void* x, int64_t ldx,
                                   veda_dtype delta_type, const void* delta, int64_t ldd, const float* weight,
                                   float eps, void* h, void* y8, float* y_scale, void* stream) {
   return norm_forward("veda_add_rms_norm_fp8", true, rows, C, x_type, x, ldx, delta_type, delta, ldd, weight, eps, h,
-                      y8, y_scale, nullptr, stream);
+                      y8, y_scale, stream);
 }
 
 veda_status veda_add_rms_norm_backward_workspace(int64_t rows, int32_t C, size_t* bytes) {
@@ -159,11 +158,12 @@ veda_status veda_add_rms_norm_backward_workspace(int64_t rows, int32_t C, size_t
 
 veda_status veda_add_rms_norm_backward(int64_t rows, int32_t C, veda_dtype x_type, const void* h,
                                        veda_dtype delta_type, const void* dy, const void* dh, const float* weight,
-                                       const float* rstd, void* dx, void* ddelta, float* dweight, void* workspace,
+                                       float eps, void* dx, void* ddelta, float* dweight, void* workspace,
                                        size_t workspace_bytes, void* stream) {
   veda_status s = check_norm(rows, C, x_type, delta_type);
   if (s != VEDA_OK) return s;
-  const void* ptrs[] = {h, dy, dh, weight, rstd, dx, ddelta, dweight, workspace};
+  if (!(eps >= 0.f) || std::isinf(eps)) return fail(VEDA_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  const void* ptrs[] = {h, dy, dh, weight, dx, ddelta, dweight, workspace};
   for (const void* p : ptrs)
     if (!aligned16(p)) return fail(VEDA_ERR_INVALID_ARG, "tensor arguments must be 16-byte aligned");
   if (rows == 0) {
@@ -173,7 +173,7 @@ veda_status veda_add_rms_norm_backward(int64_t rows, int32_t C, veda_dtype x_typ
     }
     return ok();
   }
-  if (!h || !dy || !weight || !rstd) return fail(VEDA_ERR_INVALID_ARG, "NULL tensor argument");
+  if (!h || !dy || !weight) return fail(VEDA_ERR_INVALID_ARG, "NULL tensor argument");
   if (!dx && !ddelta && !dweight) return fail(VEDA_ERR_INVALID_ARG, "no gradient is asked for");
   if (dweight) {
     const size_t need = round256(sizeof(float) * (size_t)C * add_rms_norm_bwd_parts(rows, C, sm_count()));
@@ -188,7 +188,7 @@ veda_status veda_add_rms_norm_backward(int64_t rows, int32_t C, veda_dtype x_typ
   a.dy = dy;
   a.dh = dh;
   a.w = weight;
-  a.rstd = rstd;
+  a.eps = eps;
   a.dx = dx;
   a.ddelta = ddelta;
   a.part = dweight ? static_cast<float*>(workspace) : nullptr;

@@ -11,6 +11,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <atomic>
+#include <mutex>
 #include <type_traits>
 
 #include "veda_common.cuh"
@@ -235,15 +237,30 @@ __device__ __forceinline__ float warp_sum(float v) {
 struct RowSplit {
   int cpt, W, groups, threads;
 };
-inline RowSplit row_split(int nchunk, long long rows, int sms, int most_for_two = 1024, int warps_for_two = 16) {
+inline RowSplit row_split(int nchunk, long long rows, int sms, int cpt, int most_warps = 16) {
   RowSplit r;
-  r.cpt = nchunk <= 32 ? 1 : nchunk <= most_for_two ? 2 : 4;
+  r.cpt = cpt;
   r.W = (nchunk + 32 * r.cpt - 1) / (32 * r.cpt);
-  r.groups = (r.cpt == 2 ? warps_for_two : 16) / r.W;
+  r.groups = most_warps / r.W;
   const long long each = (rows + sms - 1) / sms;   // few rows: spread them over the SMs first
   if (each < r.groups) r.groups = each < 1 ? 1 : (int)each;
   r.threads = 32 * r.W * r.groups;
   return r;
+}
+// Chunks per thread, of 1 to `most`: those that leave the fewest idle, the most
+// of them if several do (a row costs a thread some 190 instructions whatever its
+// chunks, each chunk 76, in the rotary kernel).
+inline int best_cpt(int nchunk, int most) {
+  if (nchunk <= 32) return 1;
+  int best = 0, best_slots = 0;
+  for (int cpt = 2; cpt <= most; ++cpt) {
+    const int W = (nchunk + 32 * cpt - 1) / (32 * cpt), slots = W * 32 * cpt;
+    if (W <= 16 && (best == 0 || slots <= best_slots)) {
+      best = cpt;
+      best_slots = slots;
+    }
+  }
+  return best == 0 ? 4 : best;
 }
 
 struct RowGroup {
@@ -292,18 +309,36 @@ __device__ __forceinline__ float row_sum(const RowGroup& g, float a, float* red,
   return warp_sum(g.lane < g.W ? r[g.lane] : 0.f);
 }
 
-template <typename K>
-inline cudaError_t allow_smem(K kernel, size_t smem) {
-  if (smem <= 40 * 1024) return cudaSuccess;   // what any kernel may have beside its static part
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-}
+constexpr size_t kMostSmem = 220 * 1024;   // of a CTA, beside a few KB of static shared memory
 
-// CTAs that are resident at once, so that each can keep stepping over rows.
+// A kernel's limit of dynamic shared memory, raised when a launch on that device
+// first asks for more (a call per launch is a fifth of a small call's time).  It
+// is not raised to what any launch may ever need: the driver sizes L1 by it, and
+// the norm of 75,600 x 5,120 took 498 us instead of 446 with a limit of 220 KB.
+struct PerDevice {
+  std::atomic<int> most[64] = {};
+  std::mutex raising;           // two threads must not lower each other's limit
+  template <typename K>
+  cudaError_t allow_smem(K kernel, size_t smem) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && most[dev].load(std::memory_order_acquire) >= (int)smem)) return e;
+    std::lock_guard<std::mutex> lock(raising);
+    if (dev < 64 && most[dev].load(std::memory_order_relaxed) >= (int)smem) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess && dev < 64) most[dev].store((int)smem, std::memory_order_release);
+    return e;
+  }
+};
+
+// CTAs to launch for `want` of them: at most as many as are resident at once, so
+// that each can keep stepping over rows.
 template <typename K>
-inline unsigned resident_ctas(K kernel, int threads, size_t smem, int sms) {
+inline unsigned resident_ctas(long long want, K kernel, int threads, size_t smem, int sms) {
+  if (want <= sms) return (unsigned)want;
   int n = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess || n < 1) n = 1;
-  return (unsigned)(n * sms);
+  return (unsigned)(want < (long long)n * sms ? want : (long long)n * sms);
 }
 
 // The 8-bit rule: a block's scale is s = a / 448 with a its largest magnitude,

@@ -175,11 +175,12 @@ __device__ __forceinline__ float head_sum(float v, int lanes) {
   return v;
 }
 
-// Rows in flight per group, and the thread count that register use is bounded
-// by: 20 warps are to fit an SM, 32 with one chunk each.
-__host__ __device__ constexpr int rope_bounds(int cpt) { return cpt == 1 ? 1024 : cpt == 2 ? 640 : 512; }
-__host__ __device__ constexpr int rope_depth(int cpt) { return cpt == 4 ? 3 : 4; }
+// Rows in flight per group, and the warps of a CTA, which bound the registers: as
+// many as leave the kernel all but a few of those it wants.
+__host__ __device__ constexpr int rope_depth(int cpt) { return cpt > 2 ? 3 : 4; }
 __host__ __device__ constexpr int rope_bwd_depth(int cpt) { return cpt == 4 ? 1 : 3; }
+__host__ __device__ constexpr int rope_warps(int cpt) { return cpt <= 2 ? 20 : 16; }
+constexpr int kRopeBwdWarps = 16;
 
 // A token's row on its way: chunk c of it starts at (c / lph) * sh + c % lph * 8.
 template <typename T, int CPT>
@@ -197,7 +198,7 @@ __device__ __forceinline__ void fetch_token(const RopeArgs& A, const Ring<T, CPT
 }
 
 template <typename T, int CPT, bool HALVES>
-__global__ void __launch_bounds__(rope_bounds(CPT)) qkv_rope_kernel(const __grid_constant__ RopeArgs A) {
+__global__ void __launch_bounds__(32 * rope_warps(CPT)) qkv_rope_kernel(const __grid_constant__ RopeArgs A) {
   constexpr int D = rope_depth(CPT);
   __shared__ float red[kRowRed];
   extern __shared__ uint4 ring_raw[];
@@ -289,7 +290,7 @@ __global__ void __launch_bounds__(rope_bounds(CPT)) qkv_rope_kernel(const __grid
 }
 
 template <typename T, int CPT, bool HALVES>
-__global__ void __launch_bounds__(512) qkv_rope_bwd_kernel(const __grid_constant__ RopeArgs A) {
+__global__ void __launch_bounds__(32 * kRopeBwdWarps) qkv_rope_bwd_kernel(const __grid_constant__ RopeArgs A) {
   constexpr int D = rope_bwd_depth(CPT);
   __shared__ float red[kRowRed];
   extern __shared__ uint4 ring_raw[];
@@ -451,23 +452,32 @@ __global__ void rope_table_kernel(int n, int pairs, int dim, double log2_theta, 
 
 namespace {
 
-unsigned rope_grid(int tokens, const RowSplit& r, unsigned most) {
-  const unsigned want = (unsigned)((tokens + r.groups - 1) / r.groups);
-  return want < most ? want : most;
+RowSplit rope_split(int nchunk, long long tokens, int sms, bool backward) {
+  // Backward three chunks a thread spill: 280 us instead of 214 at 32,760 tokens of 12 x 128.
+  const int cpt = best_cpt(nchunk, backward ? 2 : 4);
+  return row_split(nchunk, tokens, sms, cpt, backward ? kRopeBwdWarps : rope_warps(cpt));
 }
+long long rope_ctas(long long tokens, const RowSplit& r) { return (tokens + r.groups - 1) / r.groups; }
 
 template <typename T, int CPT, bool HALVES>
-cudaError_t rope_run(RopeArgs a, const RowSplit& r, bool backward, int sms, cudaStream_t s) {
-  const auto kernel = backward ? qkv_rope_bwd_kernel<T, CPT, HALVES> : qkv_rope_kernel<T, CPT, HALVES>;
+cudaError_t rope_run(RopeArgs a, RowSplit r, bool backward, int sms, cudaStream_t s) {
+  auto kernel = qkv_rope_kernel<T, CPT, HALVES>;
+  if constexpr (CPT != 3) {
+    if (backward) kernel = qkv_rope_bwd_kernel<T, CPT, HALVES>;
+  }
   const size_t ring = backward ? rope_bwd_depth(CPT) * (Ring<T, CPT>::kBytes + Ring<__nv_bfloat16, CPT>::kBytes)
                                : rope_depth(CPT) * Ring<T, CPT>::kBytes;
   const size_t angles = backward ? Angles<HALVES, rope_bwd_depth(CPT)>::kBytes : Angles<HALVES, rope_depth(CPT)>::kBytes;
-  const size_t smem = ring * r.threads + angles * r.groups + (HALVES ? r.threads * 9 * sizeof(float) : 0);
-  cudaError_t e = allow_smem(kernel, smem);
+  const size_t group = 32 * r.W * (ring + (HALVES ? 9 * sizeof(float) : 0)) + angles;
+  r.groups = std::min(r.groups, (int)(kMostSmem / group));
+  r.threads = 32 * r.W * r.groups;
+  const size_t smem = group * r.groups;
+  static PerDevice once[2];
+  cudaError_t e = once[backward ? 1 : 0].allow_smem(kernel, smem);
   if (e != cudaSuccess) return e;
-  unsigned most = resident_ctas(kernel, r.threads, smem, sms);
-  if (backward && most > (unsigned)(kBwdCtasPerSm * sms)) most = kBwdCtasPerSm * sms;
-  const unsigned grid = rope_grid((int)a.tokens, r, most);
+  long long want = rope_ctas(a.tokens, r);
+  if (backward) want = std::min(want, (long long)kBwdCtasPerSm * sms);
+  const unsigned grid = resident_ctas(want, kernel, r.threads, smem, sms);
   a.parts = (int)grid;
   kernel<<<grid, r.threads, smem, s>>>(a);
   e = cudaGetLastError();
@@ -488,14 +498,14 @@ template <typename T>
 cudaError_t rope_run(const RopeArgs& a, const RowSplit& r, bool backward, int sms, cudaStream_t s) {
   if (r.cpt == 1) return a.halves ? rope_run<T, 1, true>(a, r, backward, sms, s) : rope_run<T, 1, false>(a, r, backward, sms, s);
   if (r.cpt == 2) return a.halves ? rope_run<T, 2, true>(a, r, backward, sms, s) : rope_run<T, 2, false>(a, r, backward, sms, s);
+  if (r.cpt == 3) return a.halves ? rope_run<T, 3, true>(a, r, backward, sms, s) : rope_run<T, 3, false>(a, r, backward, sms, s);
   return a.halves ? rope_run<T, 4, true>(a, r, backward, sms, s) : rope_run<T, 4, false>(a, r, backward, sms, s);
 }
 
 }  // namespace
 
 cudaError_t launch_qkv_rope(RopeArgs a, int type, bool backward, int sms, cudaStream_t s) {
-  const RowSplit r = backward ? row_split(a.heads * a.d / 8, a.tokens, sms)
-                              : row_split(a.heads * a.d / 8, a.tokens, sms, 256, 20);
+  const RowSplit r = rope_split(a.heads * a.d / 8, a.tokens, sms, backward);
   a.warps = r.W;
   a.HW = a.H * a.W;
   a.head_size = (long long)a.N * a.d;
@@ -509,9 +519,7 @@ cudaError_t launch_qkv_rope(RopeArgs a, int type, bool backward, int sms, cudaSt
 }
 
 // Rows of weight-gradient partials at most, each heads*d (row norm) or d (head norm) floats.
-int qkv_rope_bwd_parts(long long tokens, int heads, int d, int sms) {
-  return (int)rope_grid((int)tokens, row_split(heads * d / 8, tokens, sms), kBwdCtasPerSm * sms);
-}
+int qkv_rope_bwd_parts(long long tokens, int sms) { return (int)std::min(tokens, (long long)kBwdCtasPerSm * sms); }
 
 cudaError_t launch_rope_table(int n, int dim, double theta, double start, double step, float* out, cudaStream_t s) {
   const long long e = (long long)n * (dim / 2);

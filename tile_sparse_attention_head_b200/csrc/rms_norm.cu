@@ -9,7 +9,8 @@
 // The norm is taken of the stored h, not of the unrounded sum: backward reads
 // h back and then works with exactly the numbers forward normalised, so the
 // weight's gradient in fp32 is not limited by a 16-bit rounding between them.
-// Sums and the statistics are fp32; h, y, dx and d_delta are rounded once.
+// rstd is computed again from h: its sum shares the other's barrier, and nothing
+// has to be kept.  Sums and the statistics are fp32; h, y, dx and d_delta are rounded once.
 //
 // Every operand is read once and written once, so HBM is the bound.  A row is
 // held in registers between the sum and the output, by a group of as many warps
@@ -93,7 +94,6 @@ __global__ void __launch_bounds__(512) add_rms_norm_kernel(const __grid_constant
       }
     }
     const float rstd = rsqrtf(row_sum(g, f2_sum(ss), red, turn) * inv_c + A.eps);
-    if (A.rstd != nullptr && g.t == 0) A.rstd[row] = rstd;
     const uint64_t rr = f2_all(rstd);
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
@@ -155,11 +155,9 @@ __global__ void __launch_bounds__(512) add_rms_norm_bwd_kernel(const __grid_cons
   };
 #pragma unroll 1
   for (int s = 0; s < D; ++s) fetch(row + s * step, s * slot_size);
-  float nrstd = row < A.rows ? A.rstd[row] : 0.f;
   for (int turn = 0, slot = 0; row < A.rows; row += step, turn ^= 1) {
     uint64_t hv[CPT][4], gv[CPT][4];
     Words<TX> dv[CPT];
-    const float rstd = nrstd;
     cp_async_wait<D - 1>();
     rh.sync();
 #pragma unroll
@@ -171,29 +169,31 @@ __global__ void __launch_bounds__(512) add_rms_norm_bwd_kernel(const __grid_cons
     rh.sync();
     fetch(row + D * step, slot);
     slot = slot + slot_size == D * slot_size ? 0 : slot + slot_size;
-    if (row + step < A.rows) nrstd = A.rstd[row + step];
-    const uint64_t rr = f2_all(rstd);
-    uint64_t ss = 0;
+    uint64_t hh = 0, gh = 0;
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
       if (g.t + i * g.tpt < nchunk) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          acc[i][k] = f2_fma(f2_mul(gv[i][k], rr), hv[i][k], acc[i][k]);
-          gv[i][k] = f2_mul(gv[i][k], w[i][k]);
-          ss = f2_fma(gv[i][k], hv[i][k], ss);
+          hh = f2_fma(hv[i][k], hv[i][k], hh);
+          gh = f2_fma(f2_mul(gv[i][k], w[i][k]), hv[i][k], gh);
         }
       }
     }
-    const float c1 = -row_sum(g, f2_sum(ss), red, turn) * inv_c * rstd * rstd;
-    const uint64_t cc = f2_all(c1);
+    float s1 = f2_sum(hh), s2 = f2_sum(gh);
+    row_sum2(g, s1, s2, red, turn);
+    const float rstd = rsqrtf(s1 * inv_c + A.eps);
+    const uint64_t rr = f2_all(rstd), cc = f2_all(-s2 * inv_c * rstd * rstd);
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
       if (g.t + i * g.tpt < nchunk) {
         uint64_t d[4] = {0, 0, 0, 0};
         if (has_dh) to_pairs(dv[i], d);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) d[k] = f2_fma(rr, f2_fma(hv[i][k], cc, gv[i][k]), d[k]);
+        for (int k = 0; k < 4; ++k) {
+          acc[i][k] = f2_fma(f2_mul(gv[i][k], rr), hv[i][k], acc[i][k]);
+          d[k] = f2_fma(rr, f2_fma(hv[i][k], cc, f2_mul(gv[i][k], w[i][k])), d[k]);
+        }
         if (VEDA_IN_BOUNDS(row < A.rows)) {
           if (has_dx) store_pairs(static_cast<TX*>(A.dx) + here + 8 * i * g.tpt, d);
           if (has_dd) store_pairs(static_cast<TD*>(A.ddelta) + here + 8 * i * g.tpt, d);
@@ -249,18 +249,20 @@ cudaError_t launch_sum_partials(const SumArgs& a, int n, cudaStream_t s) {
 
 namespace {
 
-unsigned norm_grid(long long rows, const RowSplit& r, unsigned most) {
-  const long long want = (rows + r.groups - 1) / r.groups;
-  return (unsigned)(want < (long long)most ? want : most);
+RowSplit norm_split(int C, long long rows, int sms) {
+  return row_split(C / 8, rows, sms, C <= 256 ? 1 : C <= 8192 ? 2 : 4);
 }
+long long norm_ctas(long long rows, const RowSplit& r) { return (rows + r.groups - 1) / r.groups; }
 
 template <typename TX, typename TD, int CPT, bool FP8>
 cudaError_t norm_fwd(const NormArgs& a, const RowSplit& r, int sms, cudaStream_t s) {
   const auto kernel = add_rms_norm_kernel<TX, TD, CPT, FP8>;
   const size_t smem = (size_t)norm_depth(CPT) * (Ring<TX, CPT>::kBytes + Ring<TD, CPT>::kBytes) * r.threads;
-  const cudaError_t e = allow_smem(kernel, smem);
+  static PerDevice once;
+  const cudaError_t e = once.allow_smem(kernel, smem);
   if (e != cudaSuccess) return e;
-  kernel<<<norm_grid(a.rows, r, resident_ctas(kernel, r.threads, smem, sms)), r.threads, smem, s>>>(a);
+  const unsigned grid = resident_ctas(norm_ctas(a.rows, r), kernel, r.threads, smem, sms);
+  kernel<<<grid, r.threads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -275,11 +277,11 @@ template <typename TX, typename TD, int CPT>
 cudaError_t norm_bwd(NormBwdArgs a, const RowSplit& r, int sms, cudaStream_t s) {
   const auto kernel = add_rms_norm_bwd_kernel<TX, TD, CPT>;
   const size_t smem = (size_t)norm_bwd_depth(CPT) * (2 * Ring<TX, CPT>::kBytes + Ring<TD, CPT>::kBytes) * r.threads;
-  cudaError_t e = allow_smem(kernel, smem);
+  static PerDevice once;
+  cudaError_t e = once.allow_smem(kernel, smem);
   if (e != cudaSuccess) return e;
-  unsigned most = resident_ctas(kernel, r.threads, smem, sms);
-  if (most > (unsigned)(kBwdCtasPerSm * sms)) most = kBwdCtasPerSm * sms;
-  const unsigned grid = norm_grid(a.rows, r, most);
+  const long long want = std::min(norm_ctas(a.rows, r), (long long)kBwdCtasPerSm * sms);
+  const unsigned grid = resident_ctas(want, kernel, r.threads, smem, sms);
   a.parts = (int)grid;
   kernel<<<grid, r.threads, smem, s>>>(a);
   e = cudaGetLastError();
@@ -302,7 +304,7 @@ cudaError_t norm_bwd(const NormBwdArgs& a, const RowSplit& r, int sms, cudaStrea
 }  // namespace
 
 cudaError_t launch_add_rms_norm(NormArgs a, int tx, int td, bool fp8, int sms, cudaStream_t s) {
-  const RowSplit r = row_split(a.C / 8, a.rows, sms);
+  const RowSplit r = norm_split(a.C, a.rows, sms);
   a.warps = r.W;
   if (tx == VEDA_BF16) return norm_fwd<__nv_bfloat16, __nv_bfloat16>(a, fp8, r, sms, s);
   if (tx == VEDA_FP16) return norm_fwd<__half, __half>(a, fp8, r, sms, s);
@@ -312,11 +314,11 @@ cudaError_t launch_add_rms_norm(NormArgs a, int tx, int td, bool fp8, int sms, c
 
 // Partial rows of dw at most: one per CTA.
 int add_rms_norm_bwd_parts(long long rows, int C, int sms) {
-  return (int)norm_grid(rows, row_split(C / 8, rows, sms), kBwdCtasPerSm * sms);
+  return (int)std::min(norm_ctas(rows, norm_split(C, rows, sms)), (long long)kBwdCtasPerSm * sms);
 }
 
 cudaError_t launch_add_rms_norm_bwd(NormBwdArgs a, int tx, int td, int sms, cudaStream_t s) {
-  const RowSplit r = row_split(a.C / 8, a.rows, sms);
+  const RowSplit r = norm_split(a.C, a.rows, sms);
   a.warps = r.W;
   if (tx == VEDA_BF16) return norm_bwd<__nv_bfloat16, __nv_bfloat16>(a, r, sms, s);
   if (tx == VEDA_FP16) return norm_bwd<__half, __half>(a, r, sms, s);

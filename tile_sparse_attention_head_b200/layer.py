@@ -57,7 +57,8 @@ def _dense(t: Optional[torch.Tensor], shape, dtype: Optional[torch.dtype] = None
         t = t.to(dtype)
     if t.shape != shape:
         t = t.reshape(shape)
-    t = t.contiguous()
+    if not t.is_contiguous():
+        t = t.contiguous()
     return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
@@ -68,15 +69,24 @@ def _check_stream_and_delta(x: torch.Tensor, delta: Optional[torch.Tensor]) -> N
 
 # ---------------------------------------------------------------- residual and norm
 
-def _norm_forward(x, delta, weight, eps, want_rstd):
+def _norm_forward(x, delta, weight, eps):
     """Of rows x and delta; outputs are allocated like them (dense: an empty_like of rows with gaps has none)."""
     if delta is None:
         h, y = None, torch.empty_like(x)
     else:
         h, y = torch.empty_like(x), torch.empty_like(delta)
-    rstd = x.new_empty(x.shape[0], dtype=torch.float32) if want_rstd else None
-    B.veda_add_rms_norm(x, delta, weight, eps, h, y, rstd)
-    return h, y, rstd
+    B._layer_norm_forward(x, delta, weight, eps, h, y, None)
+    return h, y
+
+
+def _once(backward):
+    """backward, with once_differentiable's guard only where a graph of the gradient is asked for (it costs several
+    microseconds a call)."""
+    guarded = once_differentiable(backward)
+
+    def run(ctx, *grads):
+        return guarded(ctx, *grads) if torch.is_grad_enabled() else backward(ctx, *grads)
+    return run
 
 
 class _AddRmsNorm(torch.autograd.Function):
@@ -85,19 +95,20 @@ class _AddRmsNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, delta, weight, eps):
         x2, d2 = _flat(x), _flat(delta)
-        h, y, rstd = _norm_forward(x2, d2, weight, eps, True)
+        h, y = _norm_forward(x2, d2, weight, eps)
         ctx.set_materialize_grads(False)
         ctx.like = None if delta is None else delta.dtype
+        ctx.eps = eps
         if h is None:
-            ctx.save_for_backward(x2 if x2.is_contiguous() else x2.contiguous(), weight, rstd)
+            ctx.save_for_backward(x2 if x2.is_contiguous() else x2.contiguous(), weight)
             return y if x.dim() == 2 else y.view(x.shape)
-        ctx.save_for_backward(h, weight, rstd)
+        ctx.save_for_backward(h, weight)
         return (h, y) if x.dim() == 2 else (h.view(x.shape), y.view(x.shape))
 
     @staticmethod
-    @once_differentiable
+    @_once
     def backward(ctx, *grads):
-        h, weight, rstd = ctx.saved_tensors
+        h, weight = ctx.saved_tensors
         dh, dy = grads if len(grads) == 2 else (None, grads[0])
         want_x, want_d, want_w, _ = ctx.needs_input_grad
         if dy is None:   # only the sum itself was used: its gradient goes to both addends
@@ -107,11 +118,8 @@ class _AddRmsNorm(torch.autograd.Function):
         same = dy.dtype is h.dtype
         dx = torch.empty_like(h) if want_x or (want_d and same) else None
         dd = torch.empty_like(dy) if want_d and not same else None
-        dw = ws = None
-        if want_w:
-            dw = torch.empty_like(weight)
-            ws = h.new_empty(B.veda_add_rms_norm_backward_workspace(*h.shape, h.get_device()), dtype=torch.uint8)
-        B.veda_add_rms_norm_backward(h, dy, dh, weight, rstd, dx, dd, dw, ws)
+        dw = torch.empty_like(weight) if want_w else None
+        B._layer_norm_backward(h, dy, dh, weight, ctx.eps, dx, dd, dw)
         if len(shape) != 2:
             dx, dd = None if dx is None else dx.view(shape), None if dd is None else dd.view(shape)
         return dx if want_x else None, (dx if same else dd) if want_d else None, dw, None
@@ -126,7 +134,7 @@ def add_rms_norm(x: torch.Tensor, delta: Optional[torch.Tensor], weight: torch.T
     is taken of the rounded h.  Differentiable in x, delta and weight."""
     _check_stream_and_delta(x, delta)
     if not _wants_grad(x, delta, weight):
-        h, y, _ = _norm_forward(_flat(x), _flat(delta), weight, eps, False)
+        h, y = _norm_forward(_flat(x), _flat(delta), weight, eps)
         if x.dim() != 2:
             h, y = None if h is None else h.view(x.shape), y.view(x.shape)
         return (x if h is None else h), y
@@ -145,7 +153,7 @@ def add_rms_norm_fp8(x: torch.Tensor, delta: Optional[torch.Tensor], weight: tor
     h = torch.empty_like(x2) if delta is not None else None
     y8 = torch.empty_like(x2, dtype=B.FP8)
     scale = x2.new_empty(((C + 127) // 128, rows), dtype=torch.float32)
-    B.veda_add_rms_norm_fp8(x2, d2, weight, eps, h, y8, scale)
+    B._layer_norm_forward(x2, d2, weight, eps, h, y8, scale)
     return x if h is None else h if x.dim() == 2 else h.view(x.shape), y8, scale
 
 
@@ -188,7 +196,7 @@ def gemm_fp8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: t
     """[M, N] = a [M, K] @ b [N, K]^T (+ bias fp32 [N]) of e4m3 operands with a scale for each block of 128."""
     _no_grad_inputs("gemm_fp8", a_scale, b_scale, bias)
     if out is None:
-        out = a.new_empty((a.shape[0], b.shape[0]), dtype=out_dtype)
+        return B._layer_gemm(a, a_scale, b, b_scale, bias, out_dtype)
     return B.veda_gemm_fp8(a, a_scale, b, b_scale, bias, out)
 
 
@@ -223,7 +231,7 @@ class _QkvNormRope(torch.autograd.Function):
         return outs
 
     @staticmethod
-    @once_differentiable
+    @_once
     def backward(ctx, *douts):
         rope = ctx.rope
         wq, wk, _, _, _, *xs = ctx.saved_tensors
