@@ -292,6 +292,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       uint64_t acc[HN / 2];
 #pragma unroll
       for (int j = 0; j < HN / 2; ++j) acc[j] = 0;
+      int m, n;
+      gemm_tile(A, t, &m, &n);
+      const int row0 = m * 256 + rank * 128 + quarter * 32, col0 = n * 256 + half * HN;
+      if (A.bias != nullptr && col0 + 4 * lane < A.N)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(A.bias + col0 + 4 * lane));
       float v[2][32];
       float sc = 0.f, nsc = 0.f;
       if (!(ok = gemm_wait(bar(GBAR_DONE + it % C::kStages), (it / C::kStages) & 1, abort, tmo))) break;
@@ -326,9 +331,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
         if (!ok) break;
         sc = nsc;
       }
-      int m, n;
-      gemm_tile(A, t, &m, &n);
-      const int row0 = m * 256 + rank * 128 + quarter * 32, col0 = n * 256 + half * HN;
       if (!ok || row0 >= A.M) continue;
 #pragma unroll
       for (int p = 0; p < HN / PC; ++p) {
