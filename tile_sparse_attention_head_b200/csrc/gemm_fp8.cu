@@ -7,11 +7,10 @@
 // tensor cores (tcgen05, kind::f8f6f4, fp32 accumulation); each block's sum
 // leaves tensor memory once and is scaled and added into fp32 registers.
 //
-// Two CTAs on neighbouring SMs (a cluster) work on one 256 x 256 tile: each
-// brings its 128 rows of A and half of B's rows, and one instruction multiplies
-// on both (cta_group::2).  So an SM takes in 32 KB per k block instead of the
-// 48 KB that a 128 x 256 tile of its own would need -- at 512 cycles of tensor
-// work per block, 64 bytes a cycle, which is what an SM can take from L2.
+// Two CTAs on neighbouring SMs (a cluster) work on one 256 x 256 tile (256 x 128
+// where there are few): each brings its 128 rows of A and half of B's rows, and
+// one instruction multiplies on both (cta_group::2).  So an SM takes in 32 KB
+// per k block instead of the 48 KB that a 128 x 256 tile of its own would need.
 //
 // Pairs stay and walk the tiles.  In each CTA a producer thread brings one
 // 128-byte-wide k block of A and B per step into a ring of shared-memory stages
@@ -98,14 +97,16 @@ __device__ __forceinline__ void umma_commit(uint32_t bar) {
 }
 }  // namespace pair
 
-// Shared memory of the main kernel.
+// Shared memory of the kernel for 256 x BN tiles.
+template <int BN>
 struct GemmCfg {
   static constexpr int kThreads = 384;
   static constexpr int kStages = 4;
-  static constexpr int kHalf = 128 * 128;             // a CTA's part of A, or of B, per stage
-  static constexpr int kOffB = kStages * kHalf;
-  static constexpr int kOffOut = 2 * kStages * kHalf; // per consumer warp two pieces of 32 rows x 128 bytes
-  static constexpr int kOffScale = kOffOut + 8 * 2 * 4096;   // [2 * stages][column half][row]
+  static constexpr int kBuffers = 512 / BN;           // of tensor memory
+  static constexpr int kA = 128 * 128, kB = BN / 2 * 128;   // a CTA's part of A and of B per stage
+  static constexpr int kOffB = kStages * kA;
+  static constexpr int kOffOut = kOffB + kStages * kB;      // per consumer warp two pieces of 32 rows x 128 bytes
+  static constexpr int kOffScale = kOffOut + 8 * 2 * 4096;  // [2 * stages][column half][row]
   static constexpr int kOffBar = kOffScale + 2 * kStages * 256 * 4;
   static constexpr int kOffMisc = kOffBar + 16 * 8;
   static constexpr size_t kSmem = 1024 + kOffMisc + 64;
@@ -114,7 +115,7 @@ struct GemmCfg {
 enum {
   GBAR_FULL = 0,    // +stage (4): both CTAs' operands and scales have come (the first CTA's barrier counts)
   GBAR_DONE = 4,    // +stage (4): its multiplications are done: the stage is free, the sums are there
-  GBAR_DFREE = 8,   // +buffer (2): both CTAs' consumers have read it (the first CTA's barrier counts)
+  GBAR_DFREE = 8,   // +buffer (2 or 4): both CTAs' consumers have read it (the first CTA's barrier counts)
 };
 
 __device__ __forceinline__ bool gemm_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t timeout_ns) {
@@ -143,11 +144,11 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& A, int t, int* m, int*
   *n = r / rows;
 }
 
-template <typename TO>
+template <int BN, typename TO>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmC, const __grid_constant__ GemmArgs A) {
-  using C = GemmCfg;
+  using C = GemmCfg<BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -164,7 +165,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       mbar_init(bar(GBAR_FULL + s), 5);
       mbar_init(bar(GBAR_DONE + s), 1);
     }
-    for (int s = 0; s < 2; ++s) mbar_init(bar(GBAR_DFREE + s), 16);
+    for (int s = 0; s < C::kBuffers; ++s) mbar_init(bar(GBAR_DFREE + s), 16);
     fence_mbar_init();
   }
   if (warp == 1) pair::tmem_alloc(smem_u32(&misc[0]), 512);
@@ -185,14 +186,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       for (int t = first_tile; ok && t < A.tiles; t += pairs) {
         int m, n;
         gemm_tile(A, t, &m, &n);
-        const int row = m * 256 + rank * 128, col = n * 256 + rank * 128;
+        const int row = m * 256 + rank * 128, col = n * BN + rank * (BN / 2);
         for (int kb = 0; kb < A.kblocks; ++kb, ++it) {
           const int st = it % C::kStages, fill = it / C::kStages;
           if (fill >= 1 && !(ok = mbar_wait(bar(GBAR_DONE + st), (fill - 1) & 1, abort, tmo))) break;
-          if (VEDA_IN_BOUNDS(m * 256 < A.M && n * 256 < A.N && kb * 128 < A.K)) {
-            if (rank == 0) mbar_arrive_expect_tx(bar(GBAR_FULL + st), 4 * C::kHalf);
-            pair::tma_load_2d(sA + st * C::kHalf, &tmA, full0 + 8 * st, kb * 128, row);
-            pair::tma_load_2d(sB + st * C::kHalf, &tmB, full0 + 8 * st, kb * 128, col);
+          if (VEDA_IN_BOUNDS(m * 256 < A.M && n * BN < A.N && kb * 128 < A.K)) {
+            if (rank == 0) mbar_arrive_expect_tx(bar(GBAR_FULL + st), 2 * (C::kA + C::kB));
+            pair::tma_load_2d(sA + st * C::kA, &tmA, full0 + 8 * st, kb * 128, row);
+            pair::tma_load_2d(sB + st * C::kB, &tmB, full0 + 8 * st, kb * 128, col);
           }
         }
       }
@@ -204,20 +205,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       for (int i = it > C::kStages ? it - C::kStages : 0; i < it && !(failed && rank); ++i)
         mbar_wait(bar((failed ? GBAR_FULL : GBAR_DONE) + i % C::kStages), (i / C::kStages) & 1, &dummy, tmo);
     } else if (warp == 1 && lane == 0 && rank == 0) {
-      constexpr uint32_t idesc = make_idesc_e4m3(256, 256);
+      constexpr uint32_t idesc = make_idesc_e4m3(256, BN);
       const uint64_t da0 = make_sdesc_sw128(sA, 16, 1024), db0 = make_sdesc_sw128(sB, 16, 1024);
       int it = 0;
       bool ok = true;
       for (int t = first_tile; ok && t < A.tiles; t += pairs) {
         for (int kb = 0; kb < A.kblocks; ++kb, ++it) {
-          const int st = it % C::kStages, buf = it & 1;
+          const int st = it % C::kStages, buf = it % C::kBuffers;
           if (!(ok = mbar_wait(bar(GBAR_FULL + st), (it / C::kStages) & 1, abort, tmo))) break;
-          if (it >= 2 && !(ok = mbar_wait(bar(GBAR_DFREE + buf), ((it >> 1) - 1) & 1, abort, tmo))) break;
+          if (it >= C::kBuffers && !(ok = mbar_wait(bar(GBAR_DFREE + buf), (it / C::kBuffers - 1) & 1, abort, tmo))) break;
           tc_fence_after();
-          const uint64_t step = (uint64_t)((st * C::kHalf) >> 4);
+          const uint64_t da = da0 + (uint64_t)((st * C::kA) >> 4), db = db0 + (uint64_t)((st * C::kB) >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            pair::umma_f8(tmem + buf * 256, da0 + step + 2 * kk, db0 + step + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+            pair::umma_f8(tmem + buf * BN, da + 2 * kk, db + 2 * kk, idesc, kk > 0 ? 1u : 0u);
           pair::umma_commit(bar(GBAR_DONE + st));
         }
       }
@@ -231,7 +232,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       // The products sa sb, one warp per column half, two k blocks at a time.
       // Slots: twice the stages.  Slot it & 7 was last used for block it - 8;
       // block it - 4 has been multiplied, so its buffer was free, so block
-      // it - 6 and all before it have been read.
+      // it - 4 - kBuffers (2 or 4) and all before it have been read.
       const int half = warp - 2;
       float* dst = reinterpret_cast<float*>(smem + C::kOffScale) + half * 128 + lane;
       const uint32_t full0 = map_rank(bar(GBAR_FULL), 0);
@@ -241,7 +242,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
         int m, n;
         gemm_tile(A, t, &m, &n);
         const int row = m * 256 + rank * 128 + lane;
-        const float* pb = A.sb + (long long)min(n * 2 + half, A.nblocks - 1) * A.kblocks;
+        const float* pb = A.sb + (long long)min(BN == 256 ? n * 2 + half : n, A.nblocks - 1) * A.kblocks;
         float next[2][4], nb[2];
         auto fetch = [&](int kb) {
 #pragma unroll
@@ -277,7 +278,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-    constexpr int HN = 128;                  // columns of this warpgroup
+    constexpr int HN = BN / 2;               // columns of this warpgroup
     constexpr int PC = 128 / sizeof(TO);     // columns of an output piece
     const int half = (warp - 4) >> 2, quarter = warp & 3;
     const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * HN);
@@ -292,35 +293,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       uint64_t acc[HN / 2];
 #pragma unroll
       for (int j = 0; j < HN / 2; ++j) acc[j] = 0;
-      int m, n;
-      gemm_tile(A, t, &m, &n);
-      const int row0 = m * 256 + rank * 128 + quarter * 32, col0 = n * 256 + half * HN;
-      if (A.bias != nullptr && col0 + 4 * lane < A.N)
-        asm volatile("prefetch.global.L1 [%0];" ::"l"(A.bias + col0 + 4 * lane));
       float v[2][32];
       float sc = 0.f, nsc = 0.f;
       if (!(ok = gemm_wait(bar(GBAR_DONE + it % C::kStages), (it / C::kStages) & 1, abort, tmo))) break;
       tc_fence_after();
       sc = scales[(it & 7) * 256];
-      tmem_ld32(t_lane + (it & 1) * 256, v[0]);
+      tmem_ld32(t_lane + it % C::kBuffers * BN, v[0]);
       for (int kb = 0; kb < A.kblocks; ++kb, ++it) {
-        const uint32_t from = t_lane + (it & 1) * 256;
+        const uint32_t from = t_lane + it % C::kBuffers * BN;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < HN / 32; ++c) {
           tmem_ld_wait32(v[c & 1]);
-          if (c < 3) {
+          if (c + 1 < HN / 32) {
             tmem_ld32(from + (c + 1) * 32, v[(c + 1) & 1]);
           } else {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(free0 + 8u * (uint32_t)(it & 1));
+            if (lane == 0) mbar_arrive_cluster(free0 + 8u * (uint32_t)(it % C::kBuffers));
             if (kb + 1 < A.kblocks) {
               const int next = it + 1;
               ok = gemm_wait(bar(GBAR_DONE + next % C::kStages), (next / C::kStages) & 1, abort, tmo);
               if (ok) {
                 tc_fence_after();
                 nsc = scales[(next & 7) * 256];
-                tmem_ld32(t_lane + (next & 1) * 256, v[0]);
+                tmem_ld32(t_lane + next % C::kBuffers * BN, v[0]);
               }
             }
           }
@@ -331,6 +327,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
         if (!ok) break;
         sc = nsc;
       }
+      int m, n;
+      gemm_tile(A, t, &m, &n);
+      const int row0 = m * 256 + rank * 128 + quarter * 32, col0 = n * BN + half * HN;
       if (!ok || row0 >= A.M) continue;
 #pragma unroll
       for (int p = 0; p < HN / PC; ++p) {
@@ -609,11 +608,11 @@ __global__ void __launch_bounds__(256, 2)
 
 namespace {
 
-template <typename TO>
+template <int BN, typename TO>
 cudaError_t gemm_run(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc, GemmArgs a, int sms,
                      cudaStream_t s) {
-  using C = GemmCfg;
-  auto kernel = gemm_fp8_kernel<TO>;
+  using C = GemmCfg<BN>;
+  auto kernel = gemm_fp8_kernel<BN, TO>;
   static PerDevice once;
   static std::atomic<int> regs{0};
   cudaError_t e = once.allow_smem(kernel, C::kSmem);
@@ -627,7 +626,7 @@ cudaError_t gemm_run(const CUtensorMap& ta, const CUtensorMap& tb, const CUtenso
   }
   if (128 * 56 + 256 * 224 > C::kThreads * regs.load(std::memory_order_relaxed)) return cudaErrorInvalidConfiguration;
   a.tiles_m = (a.M + 255) / 256;
-  a.tiles_n = (a.N + 255) / 256;
+  a.tiles_n = (a.N + BN - 1) / BN;
   a.tiles = a.tiles_m * a.tiles_n;
   kernel<<<2u * (unsigned)std::min(a.tiles, sms / 2), C::kThreads, C::kSmem, s>>>(ta, tb, tc, a);
   return cudaGetLastError();
@@ -663,13 +662,22 @@ cudaError_t gemm_launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUte
     case 16: return gemm_few_run<16, TO>(ta, tb, a, s);
     case 32: return gemm_few_run<32, TO>(ta, tb, a, s);
     case 64: return gemm_few_run<64, TO>(ta, tb, a, s);
-    default: return gemm_run<TO>(ta, tb, tc, a, sms, s);
+    default: return a.bn == 128 ? gemm_run<128, TO>(ta, tb, tc, a, sms, s) : gemm_run<256, TO>(ta, tb, tc, a, sms, s);
   }
 }
 
 }  // namespace
 
-// Chooses the kernel -- few = 0: 256 x 256 tiles; otherwise the rows per tile of
+// Columns of a tile: 128 where such tiles fit the pairs of SMs in one go, since
+// a block's chain is shorter then (us, 256 / 128 columns: 14.3 / 12.2 for 777 x
+// 2,056 x 1,552, 27.0 / 23.3 for 256 x 5,120 x 5,120); otherwise 256, since an
+// SM takes in half as much again per multiplication with 128 (12.9 / 16.7 for
+// 1,560 x 1,536 x 1,536, 142 / 218 for 5,000 x 5,120 x 5,120).
+inline int gemm_bn(int M, int N, int sms) {
+  return ((M + 255LL) / 256) * ((N + 127LL) / 128) * 2 <= sms ? 128 : 256;
+}
+
+// Chooses the kernel -- few = 0: 256 x bn tiles; otherwise the rows per tile of
 // the one for few rows -- and into how many CTAs a tile's k blocks are split.
 // Measured on 148 SMs, us at the better split, few rows / 256 x 256 tiles:
 //   M =    1: 17.3 / 32.0 (N, K = 15,360, 5,120), 10.5 / 25.3 (5,120, 5,120), 5.1 / 11.9 (1,536, 1,536)
@@ -682,6 +690,7 @@ cudaError_t gemm_launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUte
 void plan_gemm_fp8(GemmArgs* a, int sms) {
   a->few = 0;
   a->split = 1;
+  a->bn = gemm_bn(a->M, a->N, sms);
   const long long tiles64 = a->nblocks * ((a->M + 63LL) / 64);
   if (a->M > 64 && tiles64 * 9 > sms * 5LL) return;
   a->few = a->M <= 16 ? 16 : a->M <= 32 ? 32 : 64;

@@ -230,6 +230,7 @@ struct GemmArgs {
   uint64_t timeout_ns;
   int tiles_m, tiles_n, tiles;
   int few, split;               // rows per tile of the kernel for few rows (0: the other one), CTAs per tile
+  int bn;                       // columns per tile of the other one
 };
 
 cudaError_t launch_add_rms_norm(NormArgs a, int tx, int td, bool fp8, int sms, cudaStream_t s);

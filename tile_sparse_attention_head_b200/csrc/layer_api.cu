@@ -280,7 +280,7 @@ veda_status veda_gemm_fp8(int32_t M, int32_t N, int32_t K, const void* a, int64_
   veda_status s;
   const bool wide = out_type == VEDA_FP32;
   if ((s = encode_rows(CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a, lda, M, K, g.few ? g.few : 128, &ta)) != VEDA_OK ||
-      (s = encode_rows(CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, b, ldb, N, K, 128, &tb)) != VEDA_OK ||
+      (s = encode_rows(CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, b, ldb, N, K, g.few ? 128 : g.bn / 2, &tb)) != VEDA_OK ||
       (s = encode_rows(wide ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, wide ? 4 : 2, out, ldo,
                        M, N, 32, &tc)) != VEDA_OK)
     return s;
