@@ -21,10 +21,11 @@
 // their registers while the next block is multiplied.  Results leave through
 // shared memory and TMA stores, which drop what lies past M and N.
 //
-// What bounds it: under real data the power limit (the multiplications alone,
-// with the same loads, take 4.8 ms of 75,600 x 5,120 x 15,360's 6.6 ms at
-// 1.5 GHz), otherwise the adding warps' chain per block -- wait, load, add --
-// of about 1,040 cycles at 512 of tensor work.  So the chain is kept short: a
+// Measured, 75,600 x 5,120 x 15,360: 6.0 to 6.8 ms in short runs, 7.1 ms in long
+// ones (1.98 to 1.67 PFLOP/s).  What bounds it is the power limit with normal data
+// (with zeros 5.1 ms; the multiplications and loads alone 4.8 and 3.6 ms), and
+// the adding warps' chain per block -- wait, load, add -- of about 1,040 cycles
+// at 512 of tensor work.  So the chain is kept short: a
 // stage's one barrier says both that it is free and that its sums are there,
 // the scales come with the operands' barrier, and the load of the next 32
 // columns, of the next block too, is under way while 32 are added.
@@ -613,9 +614,9 @@ cudaError_t gemm_run(const CUtensorMap& ta, const CUtensorMap& tb, const CUtenso
                      cudaStream_t s) {
   using C = GemmCfg<BN>;
   auto kernel = gemm_fp8_kernel<BN, TO>;
-  static PerDevice once;
+  static SmemLimit limit;
   static std::atomic<int> regs{0};
-  cudaError_t e = once.allow_smem(kernel, C::kSmem);
+  cudaError_t e = limit.allow(kernel, C::kSmem);
   if (e != cudaSuccess) return e;
   // The register split (128 threads at 56, 256 at 224) must fit what the block
   // is launched with, or the raise would wait forever.
@@ -636,8 +637,8 @@ template <int TN, typename TO>
 cudaError_t gemm_few_run(const CUtensorMap& tx, const CUtensorMap& tw, GemmArgs a, cudaStream_t s) {
   using C = FewCfg<TN>;
   auto kernel = gemm_few_kernel<TN, TO>;
-  static PerDevice once;
-  const cudaError_t e = once.allow_smem(kernel, C::kSmem);
+  static SmemLimit limit;
+  const cudaError_t e = limit.allow(kernel, C::kSmem);
   if (e != cudaSuccess) return e;
   a.tiles_n = a.nblocks;
   a.tiles_m = (a.M + TN - 1) / TN;

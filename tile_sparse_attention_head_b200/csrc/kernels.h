@@ -145,6 +145,8 @@ cudaError_t launch_attn_bwd_dkdv(const Geometry& G, const BwdMaps<kMaxGridMaps>&
 
 // ---- operators around the attention ----
 
+unsigned long long current_context_id();   // veda_api.cu
+
 // n / d for 0 <= n < 2^31 by one multiplication.
 struct FastDiv {
   uint32_t d, mul, shift;

@@ -311,23 +311,32 @@ __device__ __forceinline__ float row_sum(const RowGroup& g, float a, float* red,
 
 constexpr size_t kMostSmem = 220 * 1024;   // of a CTA, beside a few KB of static shared memory
 
-// A kernel's limit of dynamic shared memory, raised when a launch on that device
-// first asks for more (a call per launch is a fifth of a small call's time).  It
-// is not raised to what any launch may ever need: the driver sizes L1 by it, and
-// the norm of 75,600 x 5,120 took 498 us instead of 446 with a limit of 220 KB.
-struct PerDevice {
-  std::atomic<int> most[64] = {};
-  std::mutex raising;           // two threads must not lower each other's limit
+// A kernel's limit of dynamic shared memory, raised when a launch in that
+// device's context first asks for more, and never lowered, so that threads which
+// launch with different sizes do not take each other's limit away.  It is not
+// raised at once to what any launch may ever need: the driver sizes L1 by it,
+// and the norm of 75,600 x 5,120 took 498 us instead of 446 with a limit of 220
+// KB.
+struct SmemLimit {
+  std::mutex mu;
+  unsigned long long context[64] = {};
+  int most[64] = {};
   template <typename K>
-  cudaError_t allow_smem(K kernel, size_t smem) {
+  cudaError_t allow(K kernel, size_t smem) {
     int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess || (dev < 64 && most[dev].load(std::memory_order_acquire) >= (int)smem)) return e;
-    std::lock_guard<std::mutex> lock(raising);
-    if (dev < 64 && most[dev].load(std::memory_order_relaxed) >= (int)smem) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess && dev < 64) most[dev].store((int)smem, std::memory_order_release);
-    return e;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    const unsigned long long id = current_context_id();
+    if (id != 0 && id == context[dev] && most[dev] >= (int)smem) return cudaSuccess;
+    const int want = id != 0 && id == context[dev] ? std::max(most[dev], (int)smem) : (int)smem;
+    const cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, want);
+    if (set == cudaSuccess) {
+      context[dev] = current_context_id();   // the call may have made the context
+      most[dev] = want;
+    }
+    return set;
   }
 };
 

@@ -18,6 +18,12 @@
 // The rows to come are on their way to shared memory meanwhile, so loads stay
 // in flight through the reduction's barrier and the stores.
 //
+// Measured (6,548 GB/s is the rate of a plain copy): 75,600 x 5,120 bf16 with
+// e4m3 output 438 us, 6.2 TB/s; 32,760 x 1,536, fp32 stream beside bf16: forward
+// 94 us (5.9 TB/s), backward 119 us (6.4 TB/s).  Before the arithmetic ran on
+// pairs the 8-bit form was bound by issue slots (37 instructions a channel, now
+// 21, half of them a row's fixed part).
+//
 // dw: each group sums its own rows in registers, a CTA adds its groups in shared
 // memory and writes one partial row, and a second kernel adds the partial rows,
 // all in a fixed order.  No atomics, so a rerun gives the same bits.
@@ -258,8 +264,8 @@ template <typename TX, typename TD, int CPT, bool FP8>
 cudaError_t norm_fwd(const NormArgs& a, const RowSplit& r, int sms, cudaStream_t s) {
   const auto kernel = add_rms_norm_kernel<TX, TD, CPT, FP8>;
   const size_t smem = (size_t)norm_depth(CPT) * (Ring<TX, CPT>::kBytes + Ring<TD, CPT>::kBytes) * r.threads;
-  static PerDevice once;
-  const cudaError_t e = once.allow_smem(kernel, smem);
+  static SmemLimit limit;
+  const cudaError_t e = limit.allow(kernel, smem);
   if (e != cudaSuccess) return e;
   const unsigned grid = resident_ctas(norm_ctas(a.rows, r), kernel, r.threads, smem, sms);
   kernel<<<grid, r.threads, smem, s>>>(a);
@@ -277,8 +283,8 @@ template <typename TX, typename TD, int CPT>
 cudaError_t norm_bwd(NormBwdArgs a, const RowSplit& r, int sms, cudaStream_t s) {
   const auto kernel = add_rms_norm_bwd_kernel<TX, TD, CPT>;
   const size_t smem = (size_t)norm_bwd_depth(CPT) * (2 * Ring<TX, CPT>::kBytes + Ring<TD, CPT>::kBytes) * r.threads;
-  static PerDevice once;
-  cudaError_t e = once.allow_smem(kernel, smem);
+  static SmemLimit limit;
+  cudaError_t e = limit.allow(kernel, smem);
   if (e != cudaSuccess) return e;
   const long long want = std::min(norm_ctas(a.rows, r), (long long)kBwdCtasPerSm * sms);
   const unsigned grid = resident_ctas(want, kernel, r.threads, smem, sms);

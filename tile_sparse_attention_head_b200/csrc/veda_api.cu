@@ -369,6 +369,8 @@ namespace {
 constexpr size_t kNoAllocScratchBytes = size_t(16) << 20;
 static __device__ __align__(256) float g_noalloc_scratch[kNoAllocScratchBytes / sizeof(float)];
 
+}  // namespace
+
 // Unique id of the calling thread's current CUDA context, or 0 when none is
 // current (or the driver predates cuCtxGetId).  Ids are never reused within a
 // process, so a context torn down by cudaDeviceReset and created again gets a
@@ -397,6 +399,8 @@ unsigned long long current_context_id() {
   if (get_id(ctx, &id) != CUDA_SUCCESS) return 0;
   return id;
 }
+
+namespace {
 
 // Device address of g_noalloc_scratch on the current device.  It is looked
 // up once per device and context (the host-side symbol is only a stand-in,

@@ -10,7 +10,10 @@ layer, as torch functions over the C ABI, and the attention block they form.
 ``add_rms_norm`` and ``qkv_norm_rope`` are differentiable torch ops (their
 backward runs in the library); the 8-bit forms are for inference and refuse
 inputs that ask for a gradient.  ``VedaSelfAttention`` chains the calls.
-Everything runs on the current stream of the tensors' device.
+Everything runs on the current stream of the tensors' device, and can be
+captured into a CUDA graph; a captured ``backward()`` wants, as with torch's own
+operators, that no eager graph of the same leaves is alive (torch raises
+otherwise; ``torch.autograd.grad`` has no such condition).
 """
 from __future__ import annotations
 
