@@ -448,7 +448,7 @@ typedef enum { VEDA_PAIR_INTERLEAVED = 0, VEDA_PAIR_HALVES = 1 } veda_pairing;
  * (veda_rope_table writes one; a table that starts at a later row moves the
  * grid along that axis); NULL where the axis has no channels. */
 typedef struct {
-  int32_t B, heads, d;          /* d in {64, 128}, heads in [1, VEDA_MAX_HEADS] */
+  int32_t B, heads, d;          /* d in {64, 128}, heads in [1, VEDA_MAX_HEADS]; B x grid at most 2^30 tokens */
   veda_grid grid;
   int32_t dim_t, dim_h, dim_w;
   const float* table_t;

@@ -563,6 +563,84 @@ def test_side_stream_and_capture(V):
     V.veda_sync_status()
 
 
+def test_two_streams_at_once(V):
+    """The same calls on two streams, many in flight, with different sizes (so that launches with more and less shared
+    memory alternate)."""
+    cases = []
+    for rows, C in ((700, 5120), (90, 128)):
+        x, delta, w = norm_inputs(rows, C, BF16, BF16)
+        cases.append((x, delta, w) + gemm_inputs(rows, C, 512))
+
+    def calls(c):
+        h, q, s = V.add_rms_norm_fp8(c[0], c[1], c[2])
+        return [h, q.view(torch.uint8), s, V.gemm_fp8(*c[3:7], bias=c[7])]
+
+    want = [calls(c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[] for _ in cases]
+    for _ in range(20):
+        for i, (c, st) in enumerate(zip(cases, streams)):
+            with torch.cuda.stream(st):
+                got[i].append(calls(c))
+    torch.cuda.synchronize()
+    V.veda_sync_status()
+    for i, ref in enumerate(want):
+        for g in got[i]:
+            for a, b in zip(g, ref):
+                assert torch.equal(a, b)
+
+
+def test_offsets_past_32_bits(V):
+    """More than 2^31 elements: the last rows, whose offsets do not fit 32 bits, are what they are on their own."""
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 100 GB of free device memory")
+    rows, C, tail = (1 << 18) + 24, 8192, 24
+    x = torch.zeros(rows, C, dtype=BF16, device="cuda")
+    last = rand(tail, C, t=BF16)
+    x[-tail:] = last
+    w = 1 + 0.2 * rand(C, seed=3)
+    h, y = V.add_rms_norm(x, x, w)
+    h1, y1 = V.add_rms_norm(last, last, w)
+    assert torch.equal(h[-tail:], h1) and torch.equal(y[-tail:], y1)
+    del h, y
+    leaf = x.requires_grad_()
+    g, = torch.autograd.grad(V.add_rms_norm(leaf, x.detach(), w)[1], leaf, x.detach())
+    one = last.clone().requires_grad_()
+    g1, = torch.autograd.grad(V.add_rms_norm(one, last, w)[1], one, last)
+    assert torch.equal(g[-tail:], g1)
+    del g
+    x = x.detach()
+    h, q, s = V.add_rms_norm_fp8(x, x, w)
+    h1, q1, s1 = V.add_rms_norm_fp8(last, last, w)
+    assert torch.equal(q[-tail:].view(torch.uint8), q1.view(torch.uint8)) and torch.equal(s[:, -tail:], s1)
+    _, _, b, sb, bias = gemm_inputs(8, C, 64)
+    gemm_check(V.gemm_fp8(q, s, b, sb, bias, FP32)[-tail:], q1, s1, b, sb, bias, "far rows")
+    q, s = V.quant_fp8(x)
+    q1, s1 = V.quant_fp8(last)
+    assert torch.equal(q[-tail:].view(torch.uint8), q1.view(torch.uint8)) and torch.equal(s[:, -tail:], s1)
+    del x, h, q, s
+    heads, d, grid, dims = 64, 128, (5, 256, 256), (44, 42, 42)
+    n = grid[0] * grid[1] * grid[2]
+    qkv = torch.zeros(1, n, 3, heads, d, dtype=BF16, device="cuda")
+    qkv[:, -1] = rand(1, 3, heads, d, t=BF16)
+    wq = 1 + 0.2 * rand(heads * d, seed=5)
+    tables = V.rope_tables(grid, dims)
+    at = tuple(t[-1:].contiguous() for t in tables)
+    far = qkv[:, -1:].clone().requires_grad_()
+    qkv.requires_grad_()
+    out, ref = V.qkv_norm_rope(qkv, grid, tables, wq, wq), V.qkv_norm_rope(far, (1, 1, 1), at, wq, wq)
+    for a, c in zip(out, ref):
+        assert torch.equal(a[:, :, -1], c[:, :, 0])
+    douts = [torch.zeros_like(o) for o in out]
+    for i, g in enumerate(douts):
+        g[:, :, -1] = rand(1, heads, d, seed=50 + i, t=BF16)
+    a, = torch.autograd.grad(out, qkv, douts)
+    c, = torch.autograd.grad(ref, far, [g[:, :, -1:].contiguous() for g in douts])
+    assert torch.equal(a[:, -1], c[:, 0])
+    V.veda_sync_status()
+
+
 def block_case(V, stream_type, seed=0):
     w = PRESETS["tiny"]
     p = V.Problem(w.B, w.heads, w.d, w.S, (w.T, w.H, w.W), w.tilings)

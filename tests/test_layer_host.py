@@ -138,6 +138,9 @@ def test_rope_operand_refusals(V):
         assert fwd(q=bad) != 0
     for g in (veda_grid(0, 3, 4), veda_grid(2, 3, -1), veda_grid(1 << 20, 1 << 20, 1)):
         assert fwd(r=rope(V, grid=g)) != 0
+    assert fwd(r=rope(V, B=3, grid=veda_grid(1 << 10, 1 << 10, 1 << 9))) != 0
+    with pytest.raises(ValueError, match="even"):
+        V.rope_table(4, 43)
 
     def bwd(q=ok, d_q=PTR, dq=ok, w=PTR, dw=None, ws=None, wsb=0, r=r):
         return V.LIB.veda_qkv_norm_rope_backward(R(r), BF16, None if q is None else R(q), None, w, None, d_q, None, None,

@@ -690,7 +690,7 @@ def make_rope(B: int, heads: int, d: int, grid: Sequence[int], tables: Sequence[
             raise ValueError(f"a table must be [at least {n}, pairs, 2] (got {tuple(shape)})")
         dims.append(2 * shape[1])
         ptrs.append(_at(t, "a table", _device(t, "a table"), _F32, shape) if shape[1] else None)
-    return veda_rope(B, heads, d, veda_grid(*grid), *dims, *ptrs, _PAIRINGS[pairing], _NORMS[norm], eps)
+    return veda_rope(B, heads, d, veda_grid(*map(int, grid)), *dims, *ptrs, _PAIRINGS[pairing], _NORMS[norm], eps)
 
 
 def _tokens(t: Optional[torch.Tensor], r: veda_rope, name: str, dev: int, dtype: torch.dtype, shape):

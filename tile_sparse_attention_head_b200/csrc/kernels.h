@@ -195,7 +195,7 @@ constexpr int kBwdCtasPerSm = 3;   // of the kernels that write partial rows
 
 struct RopeArgs {
   int heads, d, H, W, HW, N;
-  long long tokens;             // B * N, below 2^31
+  long long tokens;             // B * N, at most 2^30
   long long head_size;          // N * d
   FastDiv by_n, by_hw, by_w;
   float inv_n;                  // 1 / the channels of a norm

@@ -60,7 +60,7 @@ veda_status make_rope(const veda_rope* r, RopeArgs* a) {
   const long long hw = (long long)r->grid.H * r->grid.W;
   if (hw > (1LL << 30) || hw * r->grid.T > (1LL << 30)) return fail(VEDA_ERR_INVALID_ARG, "grid has too many tokens");
   const long long N = hw * r->grid.T;
-  if (N * r->B >= (1LL << 31)) return fail(VEDA_ERR_INVALID_ARG, "B x the grid exceeds 2^31 tokens");
+  if (N * r->B > (1LL << 30)) return fail(VEDA_ERR_INVALID_ARG, "B x the grid exceeds 2^30 tokens");
   if (r->norm != VEDA_NORM_NONE && r->norm != VEDA_NORM_ROW && r->norm != VEDA_NORM_HEAD)
     return fail(VEDA_ERR_INVALID_ARG, "unknown norm %d", (int)r->norm);
   if (r->pairing != VEDA_PAIR_INTERLEAVED && r->pairing != VEDA_PAIR_HALVES)

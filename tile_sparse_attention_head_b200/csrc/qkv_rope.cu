@@ -27,7 +27,7 @@
 //
 // Measured (6,548 GB/s is the rate of a plain copy): 75,600 tokens of 40 x 128
 // 930 us, 5.0 TB/s; 32,760 tokens of 12 x 128 forward 127 us (4.8 TB/s), backward
-// 215 us (3.5 TB/s).  Issue slots bound it now, 15 instructions a channel forward
+// 215 us (3.5 TB/s).  Issue slots bound it now, 16 instructions a channel forward
 // and 31 backward at 60% issue: a row costs a thread some 190 instructions
 // whatever its chunks (sums across the group, angles, addresses).  Walking
 // consecutive tokens with additions instead of divisions took more of them, and

@@ -208,6 +208,8 @@ def gemm_fp8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: t
 def rope_table(n: int, dim: int, theta: float = 10000.0, start: float = 0.0, step: float = 1.0,
                device="cuda") -> torch.Tensor:
     """(cos, sin) of n positions start + step*i for one axis of `dim` channels: fp32 [n, dim/2, 2], angles in fp64."""
+    if dim % 2:
+        raise ValueError(f"dim must be even (got {dim})")
     return B.veda_rope_table(torch.empty((n, dim // 2, 2), dtype=torch.float32, device=device), theta, start, step)
 
 
@@ -333,6 +335,8 @@ class VedaSelfAttention:
         if tuple(w_qkv.shape) != (3 * inner, C) or tuple(w_o.shape) != (C, inner):
             raise ValueError(f"w_qkv must be [{3 * inner}, {C}] and w_o [{C}, {inner}] "
                              f"(got {tuple(w_qkv.shape)} and {tuple(w_o.shape)})")
+        if C % 16:
+            raise ValueError(f"C must be a multiple of 16 for the 8-bit products (got {C})")
         self.att, self.p, self.C = attention, p, C
         self.w_qkv, self.s_qkv = quant_fp8_weight(w_qkv)
         self.w_o, self.s_o = quant_fp8_weight(w_o)
