@@ -123,6 +123,12 @@ __device__ __forceinline__ bool gemm_wait(uint32_t bar, uint32_t parity, volatil
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, timeout_ns));
 }
 
+// The limit of the waits for copies and multiplications already in flight after
+// another wait ran out: they take microseconds, whatever limit the caller set.
+__device__ __forceinline__ uint64_t drain_limit(uint64_t timeout_ns) {
+  return timeout_ns > 50000000ull ? timeout_ns : 50000000ull;
+}
+
 // Waits for the tensor-memory loads in flight, among them the one into v: what
 // follows reads v from here, not from the load.
 __device__ __forceinline__ void tmem_ld_wait32(float* v) {
@@ -204,7 +210,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       int dummy = 0;
       const bool failed = *abort != 0;
       for (int i = it > C::kStages ? it - C::kStages : 0; i < it && !(failed && rank); ++i)
-        mbar_wait(bar((failed ? GBAR_FULL : GBAR_DONE) + i % C::kStages), (i / C::kStages) & 1, &dummy, tmo);
+        mbar_wait(bar((failed ? GBAR_FULL : GBAR_DONE) + i % C::kStages), (i / C::kStages) & 1, &dummy, drain_limit(tmo));
     } else if (warp == 1 && lane == 0 && rank == 0) {
       constexpr uint32_t idesc = make_idesc_e4m3(256, BN);
       const uint64_t da0 = make_sdesc_sw128(sA, 16, 1024), db0 = make_sdesc_sw128(sB, 16, 1024);
@@ -227,7 +233,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       // multiplications in flight are waited for here, again with a limit.
       if (!ok && it > 0) {
         int dummy = 0;
-        mbar_wait(bar(GBAR_DONE + (it - 1) % C::kStages), ((it - 1) / C::kStages) & 1, &dummy, tmo);
+        mbar_wait(bar(GBAR_DONE + (it - 1) % C::kStages), ((it - 1) / C::kStages) & 1, &dummy, drain_limit(tmo));
       }
     } else if (warp >= 2) {
       // The products sa sb, one warp per column half, two k blocks at a time.
@@ -478,7 +484,7 @@ __global__ void __launch_bounds__(256, 2)
     if (*abort) {
       int dummy = 0;
       for (int i = it > C::kStages ? it - C::kStages : 0; i < it; ++i)
-        mbar_wait(bar(FBAR_FULL + i % C::kStages), (i / C::kStages) & 1, &dummy, tmo);
+        mbar_wait(bar(FBAR_FULL + i % C::kStages), (i / C::kStages) & 1, &dummy, drain_limit(tmo));
     }
   } else if (warp == 1 && lane == 0) {
     constexpr uint32_t idesc = make_idesc_e4m3(128, TN);
@@ -497,7 +503,7 @@ __global__ void __launch_bounds__(256, 2)
     }
     if (it > 0) {   // the last multiplications, also after a wait ran out
       int dummy = 0;
-      mbar_wait(bar(FBAR_DONE + (it - 1) % C::kStages), ((it - 1) / C::kStages) & 1, &dummy, tmo);
+      mbar_wait(bar(FBAR_DONE + (it - 1) % C::kStages), ((it - 1) / C::kStages) & 1, &dummy, drain_limit(tmo));
     }
   } else if (warp == 2) {
     // The products sa sb of TN rows, two blocks ahead in registers.  A slot is
