@@ -1,0 +1,80 @@
+"""What the differentiable operators hand to the library, seen on the CPU: the
+binding's calls are replaced by ones that write the arguments down."""
+import weakref
+
+import pytest
+import torch
+from torch.utils.checkpoint import checkpoint
+
+GRID, HEADS, D = (2, 3, 4), 2, 64
+N = 24
+
+
+@pytest.fixture(scope="module")
+def V():
+    import tile_sparse_attention_head_b200 as V
+    return V
+
+
+class Rope:
+    """Stands for the C struct: like the addresses in it, it keeps no tensor alive."""
+
+    def __init__(self, b, heads, d, grid, tables):
+        self.B, self.heads, self.d, self.grid = b, heads, d, grid
+        self.tables = [weakref.ref(t) for t in tables]
+
+
+@pytest.fixture
+def calls(V, monkeypatch):
+    """The backward calls made, each as what it was given; the gradients it writes are ones."""
+    seen = []
+    B = V.binding
+
+    def forward(rope, *args):
+        for t in args[-3:]:
+            t.zero_()
+
+    def backward(rope, q, k, wq, wk, d_q, d_k, d_v, dq, dk, dv, dwq, dwk, ws):
+        tables = [t() for t in rope.tables]
+        seen.append(dict(grid=rope.grid, tables=[None if t is None else t.clone() for t in tables],
+                         wrote=[n for n, t in zip(("q", "k", "v", "wq", "wk"), (dq, dk, dv, dwq, dwk)) if t is not None]))
+        for t in (dq, dk, dv, dwq, dwk):
+            if t is not None:
+                t.fill_(1)
+
+    monkeypatch.setattr(B, "make_rope", lambda b, heads, d, grid, tables, *how: Rope(b, heads, d, grid, tables))
+    monkeypatch.setattr(B, "veda_qkv_norm_rope", forward)
+    monkeypatch.setattr(B, "veda_qkv_norm_rope_backward_workspace", lambda rope, device=None: 16)
+    monkeypatch.setattr(B, "veda_qkv_norm_rope_backward", backward)
+    return seen
+
+
+def leaves():
+    return [t.requires_grad_() for t in (torch.randn(1, N, 3, HEADS, D), torch.ones(HEADS * D), torch.ones(HEADS * D))]
+
+
+def tables():
+    return tuple(torch.full((n, dim, 2), float(10 * n + dim)) for n, dim in zip(GRID, (12, 10, 10)))
+
+
+@pytest.mark.parametrize("how", ["plain", "checkpoint", "hooks"])
+def test_rope_backward_uses_the_tables_that_autograd_kept(V, calls, how):
+    """Tables that live only as long as the call: the backward's are those that autograd hands back, not the first
+    call's addresses, whose memory may be another tensor's by then."""
+    qkv, wq, wk = leaves()
+
+    def call(qkv, wq, wk):
+        return V.qkv_norm_rope(qkv, GRID, tables(), wq, wk)
+
+    if how == "checkpoint":
+        out = checkpoint(call, qkv, wq, wk, use_reentrant=False)
+    elif how == "hooks":
+        with torch.autograd.graph.saved_tensors_hooks(lambda t: t.clone(), lambda t: t):
+            out = call(qkv, wq, wk)
+    else:
+        out = call(qkv, wq, wk)
+    grads = torch.autograd.grad(out, (qkv, wq, wk), [torch.ones_like(t) for t in out])
+    assert len(calls) == 1 and tuple(calls[0]["grid"]) == GRID
+    for got, want in zip(calls[0]["tables"], tables()):
+        assert got is not None and torch.equal(got, want)
+    assert all((g == 1).all() for g in grads)

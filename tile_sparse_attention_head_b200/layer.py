@@ -225,22 +225,26 @@ class _QkvNormRope(torch.autograd.Function):
     """q, k, v in grid order from one packed tensor or from three."""
 
     @staticmethod
-    def forward(ctx, rope, tables, wq, wk, *xs):
+    def forward(ctx, rope, tables, how, wq, wk, *xs):
         q, k, v = xs[0].unbind(2) if len(xs) == 1 else xs
         shape = (rope.B, rope.heads, q.shape[1], rope.d)
         outs = tuple(q.new_empty(shape, dtype=torch.bfloat16) for _ in range(3))
         B.veda_qkv_norm_rope(rope, q, k, v, wq, wk, *outs)
-        ctx.rope, ctx.packed = rope, len(xs) == 1
+        # rope holds the tables' addresses, which are this call's: backward may get other tensors (a checkpoint computes
+        # the tables again, a hook moves them) and makes a struct of its own.
+        ctx.sizes, ctx.how, ctx.packed = (rope.B, rope.heads, rope.d), how, len(xs) == 1
         ctx.set_materialize_grads(False)
-        ctx.save_for_backward(wq, wk, *tables, *xs)     # rope points into the tables: they must stay as they are
+        ctx.save_for_backward(wq, wk, *tables, *xs)
         return outs
 
     @staticmethod
     @_once
     def backward(ctx, *douts):
-        rope = ctx.rope
-        wq, wk, _, _, _, *xs = ctx.saved_tensors
-        want_wq, want_wk, *want_x = ctx.needs_input_grad[2:]
+        wq, wk, *rest = ctx.saved_tensors
+        tables, xs = rest[:3], rest[3:]
+        grid, pairing, norm, eps = ctx.how
+        rope = B.make_rope(*ctx.sizes, grid, tables, pairing, norm, eps)
+        want_wq, want_wk, *want_x = ctx.needs_input_grad[3:]
         if ctx.packed:
             x = xs[0]
             packed = torch.empty(x.shape, dtype=x.dtype, device=x.device)
@@ -265,7 +269,7 @@ class _QkvNormRope(torch.autograd.Function):
         else:
             dwq = dwk = None
         dx = (packed if want_x[0] else None,) if ctx.packed else tuple(x if w else None for x, w in zip(dxs, want_x))
-        return (None, None, dwq, dwk) + dx
+        return (None, None, None, dwq, dwk) + dx
 
 
 def qkv_norm_rope(qkv, grid: Sequence[int], tables: Sequence[Optional[torch.Tensor]],
@@ -302,7 +306,7 @@ def qkv_norm_rope(qkv, grid: Sequence[int], tables: Sequence[Optional[torch.Tens
             raise ValueError(f"a table is on {t.device}, qkv on {xs[0].device}")
     rope = B.make_rope(b, heads, d, grid, tables, pairing, norm, eps)
     if _wants_grad(wq, wk, *xs):
-        return _QkvNormRope.apply(rope, tuple(tables), wq, wk, *xs)
+        return _QkvNormRope.apply(rope, tuple(tables), (tuple(grid), pairing, norm, eps), wq, wk, *xs)
     if len(xs) == 1:      # one allocation: with three a call on one token is a tenth slower
         outs = qkv.new_empty((3, b, heads, n, d), dtype=torch.bfloat16).unbind(0)
         B._packed_norm_rope(rope, qkv, wq, wk, outs)
