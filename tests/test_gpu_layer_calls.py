@@ -66,3 +66,90 @@ def test_gradients_of_a_step_whose_saved_tensors_move(V, how, norm):
     V.veda_sync_status()
     for i, (a, b) in enumerate(zip(other, plain)):
         assert torch.equal(a, b), i
+
+
+# ---------------------------------------------------------------- alignment
+
+def at(offset, like):
+    """An empty tensor like `like` that starts `offset` bytes past an allocation's start, and the memory around it."""
+    n = like.numel() * like.element_size()
+    room = torch.full((n + 2 * 64 + offset,), 0xA5, dtype=torch.uint8, device="cuda")
+    return room[64 + offset:64 + offset + n].view(like.dtype).view(like.shape), room
+
+
+def untouched(room, offset):
+    return bool((room[:64 + offset] == 0xA5).all()) and bool((room[-64:] == 0xA5).all())
+
+
+@pytest.mark.parametrize("C", [72, 1000, 8200])
+@pytest.mark.parametrize("tx,td", [(FP32, FP32), (FP32, BF16), (BF16, BF16)])
+@pytest.mark.parametrize("off", [16, 32, 48])
+def test_norm_outputs_on_16_byte_borders(V, off, tx, td, C):
+    """Every tensor argument may start on any 16-byte border: inputs and outputs of the norm's calls."""
+    rows = 37
+    x, delta, w = rand(rows, C, seed=1, t=tx), rand(rows, C, seed=2, t=td), rand(C, seed=3)
+    dh, dy = rand(rows, C, seed=4, t=tx), rand(rows, C, seed=5, t=td)
+
+    def run(o):
+        rooms = []
+
+        def place(t, fill=True):
+            p, room = at(o, t)
+            if fill:
+                p.copy_(t)
+            rooms.append(room)
+            return p
+        px, pd, pw = place(x), place(delta), place(w)
+        h, y, h8, y8 = (place(t, False) for t in (x, delta, x, torch.empty(rows, C, dtype=FP8)))
+        s, dx, dd, dw = (place(t, False) for t in (torch.empty(-(-C // 128), rows), x, delta, w))
+        V.veda_add_rms_norm(px, pd, pw, 1e-6, h, y)
+        V.veda_add_rms_norm_fp8(px, pd, pw, 1e-6, h8, y8, s)
+        ws = torch.empty(V.veda_add_rms_norm_backward_workspace(rows, C), dtype=torch.uint8, device="cuda")
+        V.veda_add_rms_norm_backward(h, place(dy), place(dh), pw, 1e-6, dx, dd, dw, ws)
+        V.veda_sync_status()
+        assert all(untouched(r, o) for r in rooms)
+        return h, y, h8, y8, s, dx, dd, dw
+
+    for i, (a, b) in enumerate(zip(run(off), run(0))):
+        assert same(a, b), i
+
+
+@pytest.mark.parametrize("t", [FP32, BF16])
+@pytest.mark.parametrize("pairing,norm", [("interleaved", "row"), ("halves", "head"), ("interleaved", "none")])
+@pytest.mark.parametrize("off", [16, 32])
+def test_rope_gradients_on_16_byte_borders(V, off, pairing, norm, t):
+    """Inputs, outputs and gradients of the rotary calls on any 16-byte border; one of the three gradients alone too."""
+    grid, heads, d, n = (2, 3, 5), 5, 128, 30
+    qkv = [rand(1, n, heads, d, seed=i, t=t) for i in range(3)]
+    douts = [rand(1, heads, n, d, seed=4 + i, t=BF16) for i in range(3)]
+    nw = {"row": heads * d, "head": d, "none": 0}[norm]
+    ws = [1 + 0.2 * rand(nw, seed=8 + i) for i in range(2)] if nw else [None, None]
+    tables = V.rope_tables(grid, (44, 42, 42))
+    r = V.make_rope(1, heads, d, grid, tables, pairing, norm, 1e-6)
+
+    def run(o, only=None):
+        rooms = []
+
+        def place(x, fill=True):
+            if x is None:
+                return None
+            p, room = at(o, x)
+            if fill:
+                p.copy_(x)
+            rooms.append(room)
+            return p
+        w, xs = [place(x) for x in ws], [place(x) for x in qkv]
+        outs = [place(x, False) for x in douts]
+        V.veda_qkv_norm_rope(r, *xs, *w, *outs)
+        grads = [place(x, False) if only in (None, i) else x.clone().zero_() for i, x in enumerate(qkv)]
+        dws = [place(x, False) for x in ws]
+        scratch = torch.empty(V.veda_qkv_norm_rope_backward_workspace(r), dtype=torch.uint8, device="cuda")
+        V.veda_qkv_norm_rope_backward(r, xs[0], xs[1], *w, *(place(x) for x in douts), *grads, *dws, scratch)
+        V.veda_sync_status()
+        assert all(untouched(x, o) for x in rooms)
+        return outs + grads + [x for x in dws if x is not None]
+
+    want = run(0)
+    for only in (None, 1):
+        for i, (a, b) in enumerate(zip(run(off, only), want)):
+            assert same(a, b), (only, i)

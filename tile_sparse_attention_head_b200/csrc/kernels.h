@@ -171,6 +171,7 @@ struct NormArgs {
   void* y;             // [rows, C] in delta's type, or e4m3
   float* scale;        // e4m3 only: [ceil(C/128), rows]
   int warps;           // per row
+  bool wide;           // fp32 outputs start on 32-byte borders
 };
 
 struct NormBwdArgs {
@@ -183,6 +184,7 @@ struct NormBwdArgs {
   float* part;         // [parts, C] or null
   float* dw;
   int parts, warps;
+  bool wide;           // fp32 outputs start on 32-byte borders
 };
 
 // Sums of partial rows: out[i][c] = sum_p part[i][p, c].
@@ -211,6 +213,7 @@ struct RopeArgs {
   float* part[3];
   float* dw[2];
   int parts, warps;
+  bool wide;                    // fp32 gradients start on 32-byte borders
   int order[3], n_order;        // the operands of this launch: 0 Q, 1 K, 2 V
 };
 

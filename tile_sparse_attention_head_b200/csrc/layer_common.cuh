@@ -82,18 +82,27 @@ __device__ __forceinline__ void load_pairs(const T* p, uint64_t* v) {
   for (int k = 0; k < (int)(sizeof(T) / 2); ++k) w.u[k] = reinterpret_cast<const uint4*>(p)[k];
   to_pairs(w, v);
 }
-// One store per chunk: two of 16 bytes would each touch half of every sector.
+// `wide`: every fp32 output of the launch starts on a 32-byte border (tensors
+// need 16).  Then an fp32 chunk is one store, where two of 16 bytes would each
+// touch half of every sector.
 template <typename T>
-__device__ __forceinline__ void store_words(T* p, const Words<T>& w) {
+__device__ __forceinline__ void store_words(T* p, const Words<T>& w, bool wide) {
   if constexpr (sizeof(T) == 4) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w.u[0].x), "r"(w.u[0].y),
-                 "r"(w.u[0].z), "r"(w.u[0].w), "r"(w.u[1].x), "r"(w.u[1].y), "r"(w.u[1].z), "r"(w.u[1].w));
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %9, 0;\n\t"
+        "@p st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n\t"
+        "@!p st.global.v4.b32 [%0], {%1, %2, %3, %4};\n\t"
+        "@!p st.global.v4.b32 [%0 + 16], {%5, %6, %7, %8};\n\t}" ::"l"(p), "r"(w.u[0].x), "r"(w.u[0].y),
+        "r"(w.u[0].z), "r"(w.u[0].w), "r"(w.u[1].x), "r"(w.u[1].y), "r"(w.u[1].z), "r"(w.u[1].w), "r"((int)wide)
+        : "memory");
   } else {
     *reinterpret_cast<uint4*>(p) = w.u[0];
   }
 }
 template <typename T>
-__device__ __forceinline__ void store_pairs(T* p, const uint64_t* v) { store_words(p, to_words<T>(v)); }
+__device__ __forceinline__ void store_pairs(T* p, const uint64_t* v, bool wide) { store_words(p, to_words<T>(v), wide); }
+inline bool on_32_bytes(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
 __device__ __forceinline__ void store_shared(float* p, const uint64_t* v) {
   const Words<float> w = to_words<float>(v);

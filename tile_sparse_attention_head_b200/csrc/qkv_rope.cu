@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(32 * rope_warps(CPT)) qkv_rope_kernel(const __
         const int head = head0 + i * head_step;
         if (which < 2) angles.apply(v[i], cs, 1.f, scratch, g.lane);
         if (g.t + i * g.tpt < nchunk && VEDA_IN_BOUNDS(head < A.heads && tok < A.tokens))
-          store_pairs(row + head * A.head_size, v[i]);
+          store_pairs(row + head * A.head_size, v[i], true);
       }
     }
   }
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(32 * kRopeBwdWarps) qkv_rope_bwd_kernel(const 
       for (int i = 0; i < CPT; ++i) {
         const int head = head0 + i * head_step;
         if (g.t + i * g.tpt < nchunk && VEDA_IN_BOUNDS(head < A.heads && tok < A.tokens))
-          store_pairs(row + head * dsh, gv[i]);
+          store_pairs(row + head * dsh, gv[i], A.wide);
       }
     }
     float* part = A.part[which];
@@ -521,6 +521,7 @@ cudaError_t launch_qkv_rope(RopeArgs a, int type, bool backward, int sms, cudaSt
   a.by_hw = FastDiv(a.HW);
   a.by_w = FastDiv(a.W);
   a.inv_n = 1.f / (float)(a.norm == VEDA_NORM_ROW ? a.heads * a.d : a.d);
+  a.wide = type != VEDA_FP32 || (on_32_bytes(a.dx[0]) && on_32_bytes(a.dx[1]) && on_32_bytes(a.dx[2]));
   if (type == VEDA_BF16) return rope_run<__nv_bfloat16>(a, r, backward, sms, s);
   if (type == VEDA_FP16) return rope_run<__half>(a, r, backward, sms, s);
   return rope_run<float>(a, r, backward, sms, s);

@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(512) add_rms_norm_kernel(const __grid_constant
     for (int i = 0; i < CPT; ++i) {
       to_pairs(hw[i], v[i]);
       if (g.t + i * g.tpt < nchunk) {
-        if (has_h && VEDA_IN_BOUNDS(row < A.rows)) store_words(h + 8 * i * g.tpt, hw[i]);
+        if (has_h && VEDA_IN_BOUNDS(row < A.rows)) store_words(h + 8 * i * g.tpt, hw[i], A.wide);
 #pragma unroll
         for (int k = 0; k < 4; ++k) ss = f2_fma(v[i][k], v[i][k], ss);
       }
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(512) add_rms_norm_kernel(const __grid_constant
           if ((g.lane & 15) == 0) scale[2 * g.W * i * A.rows + row] = s;
         }
       } else {
-        if (in) store_pairs(y + 8 * i * g.tpt, v[i]);
+        if (in) store_pairs(y + 8 * i * g.tpt, v[i], A.wide);
       }
     }
     h += step * A.C;
@@ -201,8 +201,8 @@ __global__ void __launch_bounds__(512) add_rms_norm_bwd_kernel(const __grid_cons
           d[k] = f2_fma(rr, f2_fma(hv[i][k], cc, f2_mul(gv[i][k], w[i][k])), d[k]);
         }
         if (VEDA_IN_BOUNDS(row < A.rows)) {
-          if (has_dx) store_pairs(static_cast<TX*>(A.dx) + here + 8 * i * g.tpt, d);
-          if (has_dd) store_pairs(static_cast<TD*>(A.ddelta) + here + 8 * i * g.tpt, d);
+          if (has_dx) store_pairs(static_cast<TX*>(A.dx) + here + 8 * i * g.tpt, d, A.wide);
+          if (has_dd) store_pairs(static_cast<TD*>(A.ddelta) + here + 8 * i * g.tpt, d, A.wide);
         }
       }
     }
@@ -312,6 +312,7 @@ cudaError_t norm_bwd(const NormBwdArgs& a, const RowSplit& r, int sms, cudaStrea
 cudaError_t launch_add_rms_norm(NormArgs a, int tx, int td, bool fp8, int sms, cudaStream_t s) {
   const RowSplit r = norm_split(a.C, a.rows, sms);
   a.warps = r.W;
+  a.wide = (tx != VEDA_FP32 || on_32_bytes(a.h)) && (td != VEDA_FP32 || fp8 || on_32_bytes(a.y));
   if (tx == VEDA_BF16) return norm_fwd<__nv_bfloat16, __nv_bfloat16>(a, fp8, r, sms, s);
   if (tx == VEDA_FP16) return norm_fwd<__half, __half>(a, fp8, r, sms, s);
   if (td == VEDA_FP32) return norm_fwd<float, float>(a, fp8, r, sms, s);
@@ -326,6 +327,7 @@ int add_rms_norm_bwd_parts(long long rows, int C, int sms) {
 cudaError_t launch_add_rms_norm_bwd(NormBwdArgs a, int tx, int td, int sms, cudaStream_t s) {
   const RowSplit r = norm_split(a.C, a.rows, sms);
   a.warps = r.W;
+  a.wide = (tx != VEDA_FP32 || on_32_bytes(a.dx)) && (td != VEDA_FP32 || on_32_bytes(a.ddelta));
   if (tx == VEDA_BF16) return norm_bwd<__nv_bfloat16, __nv_bfloat16>(a, r, sms, s);
   if (tx == VEDA_FP16) return norm_bwd<__half, __half>(a, r, sms, s);
   if (td == VEDA_FP32) return norm_bwd<float, float>(a, r, sms, s);
