@@ -141,6 +141,14 @@ __device__ __forceinline__ void tmem_ld_wait32(float* v) {
                : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld_wait16(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+               :
+               : "memory");
+}
+
 // Tile t in an order that keeps a wave's operands in L2: groups of 8 tile rows,
 // column by column inside a group.
 __device__ __forceinline__ void gemm_tile(const GemmArgs& A, int t, int* m, int* n) {
@@ -570,7 +578,12 @@ __global__ void __launch_bounds__(256, 2)
         const float4 s = s4[j];
         sc[4 * j] = s.x, sc[4 * j + 1] = s.y, sc[4 * j + 2] = s.z, sc[4 * j + 3] = s.w;
       }
-      tmem_ld_wait();
+      if constexpr (TN == 16) {
+        tmem_ld_wait16(v);
+      } else {
+#pragma unroll
+        for (int c = 0; c < TN; c += 32) tmem_ld_wait32(v + c);
+      }
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[j] = fmaf(v[j], sc[j], acc[j]);
       tc_fence_before();
