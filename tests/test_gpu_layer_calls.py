@@ -153,3 +153,37 @@ def test_rope_gradients_on_16_byte_borders(V, off, pairing, norm, t):
     for only in (None, 1):
         for i, (a, b) in enumerate(zip(run(off, only), want)):
             assert same(a, b), (only, i)
+
+
+# ---------------------------------------------------------------- many products in flight
+
+def test_products_in_flight_repeat_their_bits(V):
+    """Products of many blocks and tiles per pair of CTAs, two streams at once: each result has the first one's bits
+    (in the pair's second CTA too, whose rows are 128 to 255 of a tile), and that one is right."""
+    cases = []
+    for M, K, N, out in ((5000, 2560, 2560, BF16), (777, 1552, 2056, FP32), (3000, 1536, 1536, FP32), (2100, 144, 2048, BF16)):
+        g = torch.Generator(device="cuda").manual_seed(M)
+        a, b = (torch.randn(n, K, generator=g, device="cuda").to(FP8) for n in (M, N))
+        kb = -(-K // 128)
+        # scales that differ from row to row and block to block by powers of two
+        sa = torch.exp2(torch.randint(-4, 5, (kb, M), generator=g, device="cuda").float())
+        sb = torch.exp2(torch.randint(-4, 5, (-(-N // 128), kb), generator=g, device="cuda").float())
+        cases.append((a, sa, b, sb, out))
+        A = a.double() * sa.double().t().repeat_interleave(128, 1)[:, :K]
+        B = b.double() * sb.double().repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]
+        c = V.gemm_fp8(a, sa, b, sb, out_dtype=out)
+        # products are exact; 128 additions in a block and one multiply-add per block, 2^-23 of the magnitudes each
+        lim = torch.finfo(out).eps / 2 * (A @ B.t()).abs() + (128 + 4 * kb) * 2.0 ** -23 * (A.abs() @ B.abs().t()) * 1.01
+        assert bool(((c.double() - A @ B.t()).abs() <= lim).all())
+    want = [V.gemm_fp8(a, sa, b, sb, out_dtype=out) for a, sa, b, sb, out in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(25):
+        got = []
+        for i, (a, sa, b, sb, out) in enumerate(cases):
+            for s in streams:
+                with torch.cuda.stream(s):
+                    got.append((i, V.gemm_fp8(a, sa, b, sb, out_dtype=out)))
+        torch.cuda.synchronize()
+        assert all(torch.equal(c, want[i]) for i, c in got)
+    V.veda_sync_status()

@@ -26,9 +26,9 @@
 // (with zeros 5.1 ms; the multiplications and loads alone 4.8 and 3.6 ms), and
 // the adding warps' chain per block -- wait, load, add -- of about 1,040 cycles
 // at 512 of tensor work.  So the chain is kept short: a
-// stage's one barrier says both that it is free and that its sums are there,
-// the scales come with the operands' barrier, and the load of the next 32
-// columns, of the next block too, is under way while 32 are added.
+// stage's one barrier says that it is free, that its sums are there and that the
+// scales are, and the load of the next 32 columns, of the next block too, is
+// under way while 32 are added.
 #include "layer_common.cuh"
 #include "kernels.h"
 #undef VEDA_SRC_ID
@@ -54,12 +54,20 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-// No release at cluster scope, which waits for the thread's memory traffic (a
-// microsecond per block, measured).  What has to be ordered are tensor-memory
-// reads, by tcgen05.fence before it, and shared-memory writes that only the
-// writer's own CTA reads.
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+// A consumer warp has read a block's sums and scales: its first lane arrives at
+// the buffer's barrier in the first CTA and at the scales' barrier in its own.
+// No branch around them, and no arrival left out where one of four would do: a
+// test of the block's number cost 2% at 75,600 x 5,120 x 15,360, this 0.5%.  No release at cluster scope either, which waits for the
+// thread's memory traffic (a microsecond per block): all that the first arrival
+// has to order are tensor-memory reads, by tcgen05.fence before it.
+__device__ __forceinline__ void arrive_read(bool first, uint32_t sums_cluster_addr, uint32_t scales_bar) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %2, 0;\n\t"
+      "@p mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t"
+      "@p mbarrier.arrive.shared::cta.b64 _, [%1];\n\t}" ::"r"(sums_cluster_addr),
+      "r"(scales_bar), "r"((int)first)
+      : "memory");
 }
 
 // The pair's forms (cta_group::2) of what veda_common.cuh has for one CTA.
@@ -107,16 +115,18 @@ struct GemmCfg {
   static constexpr int kA = 128 * 128, kB = BN / 2 * 128;   // a CTA's part of A and of B per stage
   static constexpr int kOffB = kStages * kA;
   static constexpr int kOffOut = kOffB + kStages * kB;      // per consumer warp two pieces of 32 rows x 128 bytes
-  static constexpr int kOffScale = kOffOut + 8 * 2 * 4096;  // [2 * stages][column half][row]
-  static constexpr int kOffBar = kOffScale + 2 * kStages * 256 * 4;
+  static constexpr int kOffScale = kOffOut + 8 * 2 * 4096;  // [8 slots][column half][row]
+  static constexpr int kOffBar = kOffScale + 8 * 256 * 4;
   static constexpr int kOffMisc = kOffBar + 16 * 8;
   static constexpr size_t kSmem = 1024 + kOffMisc + 64;
 };
 
 enum {
-  GBAR_FULL = 0,    // +stage (4): both CTAs' operands and scales have come (the first CTA's barrier counts)
-  GBAR_DONE = 4,    // +stage (4): its multiplications are done: the stage is free, the sums are there
+  GBAR_FULL = 0,    // +stage (4): both CTAs' operands have come (the first CTA's barrier counts)
+  GBAR_DONE = 4,    // +stage (4): its multiplications are done: the stage is free, the sums are there; and so are
+                    // the products of this CTA's scales, from the warps that write them
   GBAR_DFREE = 8,   // +buffer (2 or 4): both CTAs' consumers have read it (the first CTA's barrier counts)
+  GBAR_SFREE = 12,  // +half of the scales' slots (2): this CTA's consumers have read those of four blocks
 };
 
 __device__ __forceinline__ bool gemm_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t timeout_ns) {
@@ -177,10 +187,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
   if (tid == 0) {
     misc[1] = 0;
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(bar(GBAR_FULL + s), 5);
-      mbar_init(bar(GBAR_DONE + s), 1);
+      mbar_init(bar(GBAR_FULL + s), 1);
+      mbar_init(bar(GBAR_DONE + s), 3);
     }
     for (int s = 0; s < C::kBuffers; ++s) mbar_init(bar(GBAR_DFREE + s), 16);
+    for (int s = 0; s < 2; ++s) mbar_init(bar(GBAR_SFREE + s), 4 * 8);
     fence_mbar_init();
   }
   if (warp == 1) pair::tmem_alloc(smem_u32(&misc[0]), 512);
@@ -245,12 +256,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       }
     } else if (warp >= 2) {
       // The products sa sb, one warp per column half, two k blocks at a time.
-      // Slots: twice the stages.  Slot it & 7 was last used for block it - 8;
-      // block it - 4 has been multiplied, so its buffer was free, so block
-      // it - 4 - kBuffers (2 or 4) and all before it have been read.
+      // They are written, read and freed inside a CTA, at barriers of its own
+      // (what one CTA's threads do is not ordered for the other's by a signal
+      // through the issuer).  Block it has slot it & 7; four slots are free
+      // again when the consumers have read all four.
       const int half = warp - 2;
       float* dst = reinterpret_cast<float*>(smem + C::kOffScale) + half * 128 + lane;
-      const uint32_t full0 = map_rank(bar(GBAR_FULL), 0);
       int it = 0;
       bool ok = true;
       for (int t = first_tile; ok && t < A.tiles; t += pairs) {
@@ -280,12 +291,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             if (kb + j >= A.kblocks) break;
-            const int st = it % C::kStages, fill = it / C::kStages;
+            const int st = it % C::kStages, fill = it / C::kStages, turn = it >> 3;
+            if ((it & 3) == 0 && turn >= 1 &&
+                !(ok = gemm_wait(bar(GBAR_SFREE + ((it >> 2) & 1)), (turn - 1) & 1, abort, tmo)))
+              break;
+            // This block's phase of its stage has begun.
             if (fill >= 1 && !(ok = gemm_wait(bar(GBAR_DONE + st), (fill - 1) & 1, abort, tmo))) break;
 #pragma unroll
             for (int r = 0; r < 4; ++r) dst[(it & 7) * 256 + r * 32] = v[j][r];
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(full0 + 8 * st);
+            if (lane == 0) mbar_arrive(bar(GBAR_DONE + st));
             ++it;
           }
         }
@@ -324,7 +339,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
           } else {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(free0 + 8u * (uint32_t)(it % C::kBuffers));
+            arrive_read(lane == 0, free0 + 8u * (uint32_t)(it % C::kBuffers), bar(GBAR_SFREE + ((it >> 2) & 1)));
             if (kb + 1 < A.kblocks) {
               const int next = it + 1;
               ok = gemm_wait(bar(GBAR_DONE + next % C::kStages), (next / C::kStages) & 1, abort, tmo);
