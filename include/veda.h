@@ -372,8 +372,9 @@ veda_status veda_add_rms_norm(int64_t rows, int32_t C, veda_dtype x_type, const 
 
 /* The same with y in 8 bits: y8 [rows, C] e4m3, y_scale [ceil(C/128), rows]
  * fp32.  Per row and block of 128 channels, with a the block's largest |y| or
- * 2^-100 if that is larger: y_scale = a / 448, y8 = e4m3(y / y_scale), nearest
- * even, both quotients to fp32 accuracy; the block stands for y8 * y_scale.
+ * 2^-100 if that is larger: y_scale = a * (1 / 448), y8 = e4m3(y * (448 / a)),
+ * nearest even, in fp32 with correctly rounded quotients; the block stands for
+ * y8 * y_scale.
  * A block that holds an infinity or NaN stands for NaN.  This is the inference
  * form: it has no backward. */
 veda_status veda_add_rms_norm_fp8(int64_t rows, int32_t C, veda_dtype x_type, const void* x, int64_t ldx,

@@ -187,3 +187,64 @@ def test_products_in_flight_repeat_their_bits(V):
         torch.cuda.synchronize()
         assert all(torch.equal(c, want[i]) for i, c in got)
     V.veda_sync_status()
+
+
+# ---------------------------------------------------------------- the 8-bit rule
+
+def rule(x, per_row=True):
+    """The 8-bit rule in fp32 on the host, bit for bit: bytes and scales of blocks of 128 channels (and rows)."""
+    x = x.float().cpu().numpy()
+    R, C = x.shape
+    q, nb = np.empty((R, C), np.float32), -(-C // 128)
+    s = np.empty((nb, R) if per_row else (-(-R // 128), nb), np.float32)
+    for j in range(nb):
+        for i in range(0, R, R if per_row else 128):
+            b = x[i:i + (R if per_row else 128), 128 * j:128 * j + 128]
+            a = np.abs(b).max(1, keepdims=True) if per_row else np.abs(b).max(keepdims=True)
+            a = np.maximum(a, np.float32(2.0 ** -100))
+            q[i:i + len(b), 128 * j:128 * j + 128] = b * (np.float32(448) / a)
+            (s[j:j + 1] if per_row else s[i // 128, j:j + 1])[...] = (a * (np.float32(1) / np.float32(448))).ravel()
+    return torch.from_numpy(np.clip(q, -448, 448)).to(FP8), torch.from_numpy(s)
+
+
+def midpoints(rows, C, seed=0):
+    """Rows whose values lie on the borders between neighbouring e4m3 values once they are scaled, all exact: the
+    largest of a block is 448 times a power of two."""
+    g = np.random.default_rng(seed)
+    grid = np.arange(0x08, 0x7E, dtype=np.uint8)
+    grid = torch.from_numpy(grid).view(FP8).float().numpy()
+    mid = (grid[1:] + grid[:-1]) / 2
+    x = g.choice(np.concatenate((mid, grid)), (rows, C)) * g.choice([-1.0, 1.0], (rows, C))
+    x[:, ::128] = 448
+    return torch.from_numpy((x * np.exp2(g.integers(-20, 20, (rows, 1)))).astype(np.float32)).cuda()
+
+
+@pytest.mark.parametrize("t", [FP32, BF16, FP16])
+def test_quantisers_keep_the_rule_bit_for_bit(V, t):
+    """448 / a is correctly rounded and multiplied once: no byte differs from the rule in fp32, on random rows and on
+    the borders between e4m3 values (which bf16 and fp16 hold exactly too, within fp16's range)."""
+    mid = midpoints(130, 264)
+    rnd = rand(4000, 1000, seed=1) * torch.exp(2 * rand(4000, 1, seed=2))
+    for x in (mid if t is not FP16 else mid.clamp(-448 * 64, 448 * 64) / 64, rnd):
+        x = x.to(t)
+        q, s = V.quant_fp8(x)
+        rq, rs = rule(x)
+        assert same(q.cpu(), rq) and same(s.cpu(), rs)
+        q, s = V.quant_fp8_weight(x)
+        rq, rs = rule(x, per_row=False)
+        assert same(q.cpu(), rq) and same(s.cpu(), rs)
+    o = rand(2, 3, 500, 64, seed=3, t=t)
+    q, s = V.quant_fp8_heads(o)
+    rq, rs = rule(o.transpose(1, 2).reshape(1000, 192))
+    assert same(q.cpu(), rq) and same(s.cpu(), rs)
+
+
+@pytest.mark.parametrize("rows,C", [(8192, 4096), (3000, 1000), (501, 256), (300, 8200)])
+def test_norm_and_quantiser_have_one_rule(V, rows, C):
+    """With an fp32 stream the norm's fp32 output, quantised, is its 8-bit output: the same bytes and scales."""
+    x, delta, w = rand(rows, C, seed=1), rand(rows, C, seed=2, scale=0.3), 1 + 0.2 * rand(C, seed=3)
+    h, y = V.add_rms_norm(x, delta, w)
+    h8, q, s = V.add_rms_norm_fp8(x, delta, w)
+    q2, s2 = V.quant_fp8(y)
+    assert same(h, h8) and same(s, s2)
+    assert same(q, q2), int((q.view(torch.uint8) != q2.view(torch.uint8)).sum())

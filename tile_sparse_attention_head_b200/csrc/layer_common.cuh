@@ -359,24 +359,17 @@ inline unsigned resident_ctas(long long want, K kernel, int threads, size_t smem
   return (unsigned)(want < (long long)n * sms ? want : (long long)n * sms);
 }
 
-// The 8-bit rule: a block's scale is s = a / 448 with a its largest magnitude,
-// but at least 2^-100 (so that a block of zeros has a scale and 1 / s stays
-// finite), and the block holds e4m3(x / s), nearest even.  The scale is a
-// product with 1 / 448; the norm multiplies by an approximate reciprocal of it
-// (full divisions, twice per 8 channels, were a fifth of its instructions), the
-// quantisers by 448 / a.  The maximum
-// passes NaN on: a block with an infinity or NaN gets a scale that is infinite
-// or NaN, and stands for NaN as a whole, rather than for a finite wrong value.
+// The 8-bit rule, the norm's and the quantisers' alike: with a a block's largest
+// magnitude, but at least 2^-100 (so that a block of zeros has a scale and the
+// factor stays finite), its scale is a * (1 / 448) and it holds e4m3(x * f),
+// nearest even, with f = 448 / a correctly rounded.  The maximum passes NaN on: a
+// block with an infinity or NaN gets a scale that is infinite or NaN, and
+// stands for NaN as a whole, rather than for a finite wrong value.
 constexpr float kE4M3Max = 448.f;
 constexpr float kTiny = 7.888609052210118e-31f;   // 2^-100
 
 __device__ __forceinline__ float e4m3_scale(float a) { return a * (1.f / 448.f); }
-// Of a scale: between 2^-109 and 2^120, so its reciprocal is a normal number.
-__device__ __forceinline__ float reciprocal(float s) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
-  return r;
-}
+__device__ __forceinline__ float e4m3_factor(float a) { return kE4M3Max / a; }
 
 __device__ __forceinline__ float max_nan(float a, float b) {
   float d;

@@ -112,10 +112,9 @@ __global__ void __launch_bounds__(512) add_rms_norm_kernel(const __grid_constant
         if (in) a = max_abs(a, v[i]);
 #pragma unroll
         for (int off = 8; off; off >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, off));
-        const float s = e4m3_scale(a);
         if (in) {
-          *reinterpret_cast<uint2*>(y + 8 * i * g.tpt) = to_e4m3(v[i], reciprocal(s));
-          if ((g.lane & 15) == 0) scale[2 * g.W * i * A.rows + row] = s;
+          *reinterpret_cast<uint2*>(y + 8 * i * g.tpt) = to_e4m3(v[i], e4m3_factor(a));
+          if ((g.lane & 15) == 0) scale[2 * g.W * i * A.rows + row] = e4m3_scale(a);
         }
       } else {
         if (in) store_pairs(y + 8 * i * g.tpt, v[i], A.wide);
