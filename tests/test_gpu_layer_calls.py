@@ -248,3 +248,35 @@ def test_norm_and_quantiser_have_one_rule(V, rows, C):
     q2, s2 = V.quant_fp8(y)
     assert same(h, h8) and same(s, s2)
     assert same(q, q2), int((q.view(torch.uint8) != q2.view(torch.uint8)).sum())
+
+
+# ---------------------------------------------------------------- the attention block
+
+def test_attention_blocks_on_an_fp16_stream(V):
+    """Two blocks in a row on an fp16 residual stream: the first one's output (bf16) is the second one's delta."""
+    from parity import mlp_device
+    from veda_synth import PRESETS, make_mlp
+    w = PRESETS["tiny"]
+    p = V.Problem(w.B, w.heads, w.d, w.S, (w.T, w.H, w.W), w.tilings)
+    C, inner = 640, w.heads * w.d
+    mlp = mlp_device(make_mlp(w, seed=1))
+    att = V.VedaAttention(p, mlp, mlp, w.keep)
+    tables = V.rope_tables(p.grid, (w.d // 4, 3 * w.d // 8, 3 * w.d // 8))
+    nw, ones = 1 + 0.2 * rand(C, seed=2), torch.ones(inner, device="cuda")
+    block = V.VedaSelfAttention(att, rand(3 * inner, C, seed=3, scale=C ** -0.5, t=FP16),
+                                rand(C, inner, seed=4, scale=inner ** -0.5, t=FP16), nw, tables, ones, ones)
+    x, delta = rand(p.B, p.N, C, seed=5, t=FP16), None
+    for _ in range(2):
+        h, out = block(x, delta)
+        V.veda_sync_status()
+        assert h.dtype == FP16 and out.dtype == BF16 and h.shape == out.shape == x.shape
+        want = x if delta is None else (x.float() + delta.float()).half()
+        # one rounding, and 2^-25 more where the delta is below fp16's normal range
+        assert bool(((h.float() - want.float()).abs() <= 2.0 ** -24 + want.float().abs() * 2.0 ** -11).all())
+        _, y8, ys = V.add_rms_norm_fp8(h, None, nw)
+        qkv = V.gemm_fp8(y8, ys, block.w_qkv, block.s_qkv)
+        q, k, v = V.qkv_norm_rope(qkv.view(p.B, p.N, 3, p.heads, p.d), p.grid, tables, ones, ones)
+        o8, os = V.quant_fp8_heads(att(q, k, v))
+        assert torch.equal(out, V.gemm_fp8(o8, os, block.w_o, block.s_o).view(out.shape))
+        assert bool(torch.isfinite(out).all())
+        x, delta = h, out

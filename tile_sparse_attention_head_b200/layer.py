@@ -326,8 +326,10 @@ class VedaSelfAttention:
     ``attention`` is a VedaAttention; weights are given in bf16, fp16 or fp32
     and laid out in e4m3 once: w_qkv [3*heads*d, C], w_o [C, heads*d], biases fp32
     or None, norm_weight [C], wq and wk the Q/K norm's weights (see qkv_norm_rope).
-    The residual stream goes through unchanged in type; ``out`` (bf16) is the
-    delta of the next block."""
+    The residual stream x is bf16, fp16 or fp32 and goes through unchanged in
+    type; ``out`` (bf16) is the delta of the next block.  With an fp16 stream a
+    bf16 delta is brought to fp16 first: exact in fp16's normal range, to its
+    step 2^-24 below, infinite above."""
 
     def __init__(self, attention, w_qkv: torch.Tensor, w_o: torch.Tensor, norm_weight: torch.Tensor,
                  tables: Sequence[Optional[torch.Tensor]], wq: Optional[torch.Tensor] = None,
@@ -362,6 +364,8 @@ class VedaSelfAttention:
 
     def _run(self, x, delta):
         p = self.p
+        if delta is not None and x.dtype is torch.float16 and delta.dtype is torch.bfloat16:
+            delta = delta.to(torch.float16)
         h, y, ys = add_rms_norm_fp8(x, delta, self.norm_weight, self.eps)
         qkv = gemm_fp8(y, ys, self.w_qkv, self.s_qkv, self.b_qkv)
         q, k, v = qkv_norm_rope(qkv.view(p.B, p.N, 3, p.heads, p.d), p.grid, self.tables, self.wq, self.wk, self.norm,
