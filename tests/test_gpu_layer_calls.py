@@ -280,3 +280,24 @@ def test_attention_blocks_on_an_fp16_stream(V):
         assert torch.equal(out, V.gemm_fp8(o8, os, block.w_o, block.s_o).view(out.shape))
         assert bool(torch.isfinite(out).all())
         x, delta = h, out
+
+
+def test_inputs_at_any_element(V):
+    """The torch functions take rows that start at any element, with gradients too."""
+    x, delta, w = rand(33, 200, seed=1, t=BF16), rand(33, 200, seed=2, t=BF16), 1 + 0.2 * rand(200, seed=3)
+    dy = rand(33, 200, seed=4, t=BF16)
+
+    def odd(t):
+        p = torch.empty(t.numel() + 3, dtype=t.dtype, device="cuda")[3:].view(t.shape)
+        return p.copy_(t)
+
+    def run(put):
+        leaves = [put(x).requires_grad_(), put(delta).requires_grad_(), w.clone().requires_grad_()]
+        h, y = V.add_rms_norm(*leaves)
+        g = torch.autograd.grad((h, y), leaves, (dy, put(dy)))
+        with torch.no_grad():
+            return [h, y, *g, *V.add_rms_norm_fp8(*leaves), *V.quant_fp8(put(x)), *V.quant_fp8(put(x).view(3, 11, 200))]
+
+    for i, (a, b) in enumerate(zip(run(odd), run(lambda t: t.clone()))):
+        assert same(a, b), i
+    V.veda_sync_status()

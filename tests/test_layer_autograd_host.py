@@ -78,3 +78,27 @@ def test_rope_backward_uses_the_tables_that_autograd_kept(V, calls, how):
     for got, want in zip(calls[0]["tables"], tables()):
         assert got is not None and torch.equal(got, want)
     assert all((g == 1).all() for g in grads)
+
+
+# ---------------------------------------------------------------- rows as the library reads them
+
+@pytest.mark.parametrize("offset", [0, 1, 4, 8, 12])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_rows_are_laid_out_as_the_library_reads_them(V, dtype, offset):
+    """Aligned rows are read in place; what is unaligned, overlapping or strided otherwise is copied."""
+    base = torch.randn(64 * 1024).to(dtype)
+    assert base.data_ptr() % 64 == 0
+    aligned = offset * base.element_size() % 16 == 0
+    cases = [(base[offset:offset + 24 * 64].view(24, 64), True),
+             (base[offset:offset + 24 * 64].view(2, 3, 4, 64), True),
+             (base[:24 * 96].view(24, 96)[:, offset:offset + 64], True),
+             (base[offset:offset + 64], True),
+             (base[offset:offset + 64].expand(24, 64), False),
+             (base[offset:offset + 64 * 24].view(64, 24).t(), False),
+             (base[:24 * 100].view(24, 100)[:, offset:offset + 64], False)]
+    for t, in_place in cases:
+        f = V.layer._flat(t)
+        assert f.shape == (t.numel() // t.shape[-1], t.shape[-1]) and f.data_ptr() % 16 == 0
+        assert torch.equal(f.reshape(t.shape), t)
+        assert f.stride(1) == 1 and (f.stride(0) % 8 == 0 and f.stride(0) >= f.shape[1] or f.shape[0] == 1)
+        assert (f.data_ptr() == t.data_ptr()) == (in_place and aligned)

@@ -40,16 +40,18 @@ def _no_grad_inputs(func: str, *tensors) -> None:
 
 def _flat(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
     """[..., C] as rows [R, C] that the library can read in place: contiguous channels, 16-byte aligned rows that do
-    not overlap; a copy only where the tensor is not like that (a broadcast one, say)."""
+    not overlap; a copy only where the tensor is not like that (a broadcast one, or one that starts elsewhere)."""
     if t is None:
         return None
     if t.dim() != 2:
         t = t.reshape(t.numel() // t.shape[-1] if t.dim() and t.shape[-1] else 0, t.shape[-1] if t.dim() else 0)
+    aligned = t.data_ptr() % 16 == 0
     if t.is_contiguous():
-        return t
+        return t if aligned else t.clone()
     rows, C = t.shape
     stride, step = t.stride()
-    return t if (step == 1 or C == 1) and (rows == 1 or (stride >= C and stride % 8 == 0)) else t.contiguous()
+    fits = aligned and (step == 1 or C == 1) and (rows == 1 or (stride >= C and stride % 8 == 0))
+    return t if fits else t.contiguous()
 
 
 def _dense(t: Optional[torch.Tensor], shape, dtype: Optional[torch.dtype] = None) -> Optional[torch.Tensor]:
