@@ -301,3 +301,30 @@ def test_inputs_at_any_element(V):
     for i, (a, b) in enumerate(zip(run(odd), run(lambda t: t.clone()))):
         assert same(a, b), i
     V.veda_sync_status()
+
+
+@pytest.mark.parametrize("packed", [True, False])
+@pytest.mark.parametrize("norm", ["row", "head"])
+def test_gradients_of_some_rotary_inputs_alone(V, norm, packed):
+    """The gradients of the weights alone, of one operand alone, and of one output alone are the full step's."""
+    grid, heads, d = (2, 3, 5), 3, 64
+    nw = heads * d if norm == "row" else d
+    qkv = rand(2, 30, 3, heads, d, seed=1, t=BF16)
+    xs = [qkv] if packed else [t.clone() for t in qkv.unbind(2)]
+    ws = [1 + 0.2 * rand(nw, seed=2), 1 + 0.2 * rand(nw, seed=3)]
+    douts = [rand(2, heads, 30, d, seed=4 + i, t=BF16) for i in range(3)]
+    tables = V.rope_tables(grid, (24, 20, 20))
+
+    def grads(which, used=(0, 1, 2)):
+        leaves = [t.clone().requires_grad_(i in which) for i, t in enumerate(xs + ws)]
+        out = V.qkv_norm_rope(leaves[0] if packed else leaves[:3], grid, tables, *leaves[-2:], norm=norm)
+        return torch.autograd.grad([out[i] for i in used], [leaves[i] for i in which], [douts[i] for i in used])
+
+    n = len(xs)
+    full = grads(range(n + 2))
+    for which in ([n], [n + 1], [n, n + 1], [0], [n - 1], [0, n + 1]):
+        for i, g in zip(which, grads(which)):
+            assert torch.equal(g, full[i]), (which, i)
+    g, = grads([n], used=(0,))
+    assert torch.equal(g, full[n])
+    V.veda_sync_status()

@@ -102,3 +102,42 @@ def test_rows_are_laid_out_as_the_library_reads_them(V, dtype, offset):
         assert torch.equal(f.reshape(t.shape), t)
         assert f.stride(1) == 1 and (f.stride(0) % 8 == 0 and f.stride(0) >= f.shape[1] or f.shape[0] == 1)
         assert (f.data_ptr() == t.data_ptr()) == (in_place and aligned)
+
+
+# ---------------------------------------------------------------- what a backward goes through
+
+@pytest.mark.parametrize("packed", [True, False])
+@pytest.mark.parametrize("wants,used,wrote", [
+    ("q k v wq wk", "qkv", ["q", "k", "v", "wq", "wk"]), ("q k v wq wk", "k", ["k", "wk"]),
+    ("q k v", "qkv", ["q", "k", "v"]), ("wq", "qkv", ["q", "wq"]), ("wq wk", "qkv", ["q", "k", "wq", "wk"]),
+    ("wk", "kv", ["k", "wk"])])
+def test_rope_backward_leaves_out_what_no_one_asked_for(V, calls, packed, wants, used, wrote):
+    """Frozen operands or weights, and outputs that are not used, take no part in the backward call."""
+    qkv, wq, wk = leaves()
+    xs = [qkv] if packed else [x.detach().clone() for x in qkv.unbind(2)]
+    for t, n in zip((*xs, wq, wk), (("q",) if packed else ("q", "k", "v")) + ("wq", "wk")):
+        t.requires_grad_(n in wants.split())
+    out = V.qkv_norm_rope(xs[0] if packed else xs, GRID, tables(), wq, wk)
+    out = [t for t, n in zip(out, "qkv") if n in used]
+    ask = [t for t in (*xs, wq, wk) if t.requires_grad]
+    grads = torch.autograd.grad(out, ask, [torch.ones_like(t) for t in out], allow_unused=True)
+    assert [c["wrote"] for c in calls] == [wrote]
+    for t, g in zip(ask, grads):
+        if t is qkv:
+            assert all((g[:, :, i] == (1 if n in used else 0)).all() for i, n in enumerate("qkv"))
+        else:
+            name = "wq" if t is wq else "wk" if t is wk else "qkv"[[x is t for x in xs].index(True)]
+            assert g is None if name[-1] not in used else (g == 1).all()
+
+
+def test_rope_backward_of_frozen_operands(V, calls):
+    """Only v wants a gradient: q and k are not gone through; no output is used that a leaf depends on: no call."""
+    xs = [x.detach().clone() for x in leaves()[0].unbind(2)]
+    xs[2].requires_grad_()
+    wq, wk = torch.ones(HEADS * D), torch.ones(HEADS * D)
+    out = V.qkv_norm_rope(xs, GRID, tables(), wq, wk)
+    g, = torch.autograd.grad(out, xs[2], [torch.ones_like(t) for t in out])
+    assert calls[0]["wrote"] == ["v"] and (g == 1).all()
+    out = V.qkv_norm_rope(xs, GRID, tables(), wq, wk)
+    assert torch.autograd.grad(out[0], xs[2], torch.ones_like(out[0]), allow_unused=True) == (None,)
+    assert len(calls) == 1

@@ -247,20 +247,22 @@ class _QkvNormRope(torch.autograd.Function):
         grid, pairing, norm, eps = ctx.how
         rope = B.make_rope(*ctx.sizes, grid, tables, pairing, norm, eps)
         want_wq, want_wk, *want_x = ctx.needs_input_grad[3:]
-        if ctx.packed:
-            x = xs[0]
-            packed = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        q, k, v = xs[0].unbind(2) if ctx.packed else xs
+        want = want_x * 3 if ctx.packed else want_x
+        # An operand is gone through for its own gradient or its weight's (its own is written then all the same).
+        need = [g is not None and (w or ww) for g, w, ww in zip(douts, want, (want_wq, want_wk, False))]
+        packed = None
+        if ctx.packed and want[0]:
+            packed = torch.empty(xs[0].shape, dtype=q.dtype, device=q.device)
             for i, g in enumerate(douts):
                 if g is None:
                     packed[:, :, i].zero_()
-            q, k, v = x.unbind(2)
             dxs = list(packed.unbind(2))
         else:
-            q, k, v = xs
-            dxs = [None if g is None else torch.empty(q.shape, dtype=q.dtype, device=q.device) for g in douts]
-        need = [g is not None for g in douts]
+            dxs = [torch.empty(q.shape, dtype=q.dtype, device=q.device) if n else None for n in need]
         if any(need):
-            d = [_dense(g, (rope.B, rope.heads, q.shape[1], rope.d), torch.bfloat16) for g in douts]
+            shape = (rope.B, rope.heads, q.shape[1], rope.d)
+            d = [_dense(g, shape, torch.bfloat16) if n else None for g, n in zip(douts, need)]
             dwq = torch.empty_like(wq) if want_wq and need[0] else None
             dwk = torch.empty_like(wk) if want_wk and need[1] else None
             ws = None
@@ -270,7 +272,7 @@ class _QkvNormRope(torch.autograd.Function):
                                           dwq, dwk, ws)
         else:
             dwq = dwk = None
-        dx = (packed if want_x[0] else None,) if ctx.packed else tuple(x if w else None for x, w in zip(dxs, want_x))
+        dx = (packed,) if ctx.packed else tuple(x if w else None for x, w in zip(dxs, want_x))
         return (None, None, None, dwq, dwk) + dx
 
 
