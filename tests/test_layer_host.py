@@ -250,3 +250,42 @@ def test_oracle_rope_gradient_against_differences(norm, halves):
     if w is not None:
         assert np.abs(differences(loss, w) - dw).max() < 1e-7
         assert np.all(np.abs(dw) <= magw * (1 + 1e-12))
+
+
+# ---------------------------------------------------------------- sizes past 32 bits
+
+def test_sizes_past_32_bits_are_refused(V, monkeypatch):
+    """ctypes passes the low 32 bits of a size that does not fit: each such size is refused before any call.  The
+    tensors are broadcast, so nothing of their size is allocated."""
+    B = V.binding
+    made = []
+    monkeypatch.setattr(B, "_device", lambda t, name: t.get_device())
+    monkeypatch.setattr(B, "_call", lambda *a: made.append(a[0]))
+    monkeypatch.setattr(B, "_at", lambda *a: PTR)
+    monkeypatch.setattr(B, "_rows", lambda *a: (PTR, 64))
+    big = (1 << 32) + 64
+    f8, one = torch.zeros(1, 1, dtype=torch.float8_e4m3fn), torch.zeros(1, 1, dtype=torch.bfloat16)
+    s = torch.ones(1, 1)
+    x = one.expand(1, big)
+    calls = [lambda: V.veda_gemm_fp8(f8.expand(big, 64), s, f8.expand(64, 64), s, None, one.expand(big, 64)),
+             lambda: V.veda_gemm_fp8(f8.expand(64, 64), s, f8.expand(big, 64), s, None, one.expand(64, big)),
+             lambda: V.gemm_fp8(f8.expand(big, 64), s, f8.expand(64, 64), s),
+             lambda: V.gemm_fp8(f8.expand(64, big), s, f8.expand(64, big), s),
+             lambda: V.veda_add_rms_norm(x, None, s, 1e-6, None, x),
+             lambda: V.veda_add_rms_norm_fp8(x, None, s, 1e-6, None, f8, s),
+             lambda: V.binding._layer_norm_forward(x, None, s, 1e-6, None, x, None),
+             lambda: V.veda_quant_fp8_weight(one.expand(big, 64), f8, s),
+             lambda: V.veda_quant_fp8_weight(x, f8, s),
+             lambda: V.veda_quant_fp8(one.view(1, 1, 1, 1).expand(big, 1, 1, 1), f8, s),
+             lambda: V.veda_quant_fp8(one.view(1, 1, 1, 1).expand(1, big, 1, 1), f8, s),
+             lambda: V.veda_rope_table(s.view(1, 1, 1).expand(big, 16, 2)),
+             lambda: V.veda_add_rms_norm_backward(x, x, None, s, 1e-6, x, None, None, None),
+             lambda: V.veda_add_rms_norm_backward_workspace(4, big),
+             lambda: V.make_rope(1, 2, 64, (big, 1, 1), (None, None, None)),
+             lambda: V.make_rope(big, 2, 64, (1, 1, 1), (None, None, None)),
+             lambda: V.make_rope(1, big, 64, (1, 1, 1), (None, None, None))]
+    for i, call in enumerate(calls):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
+            raise AssertionError(f"call {i} was made")
+    assert made == []

@@ -477,6 +477,11 @@ def _rows(t: Optional[torch.Tensor], name: str, dev: int, shape=None) -> Tuple[O
     return t.data_ptr(), t.stride(0) if size[0] > 1 else size[1]
 
 
+def _too_large(*sizes: int) -> None:
+    """Refuses sizes that the library's 32-bit arguments cannot hold (ctypes would pass their low 32 bits)."""
+    raise ValueError(f"a size in {sizes} does not fit 32 bits")
+
+
 def _call(func: str, dev: int, stream, *args) -> None:
     """Runs the library function with `dev` current, on `stream` or that device's current stream."""
     if dev != torch._C._cuda_getDevice():
@@ -500,6 +505,8 @@ def veda_add_rms_norm(x: torch.Tensor, delta: Optional[torch.Tensor], weight: to
     """h = x + delta and its RMS norm y, [rows, C]; y is of delta's type (x's without a delta)."""
     dev, shape = _device(x, "x"), x.shape
     xp, ldx = _rows(x, "x", dev)
+    if shape[1] >> 31:
+        _too_large(shape[1])
     dp, ldd = _rows(delta, "delta", dev, shape)
     td = y.dtype if delta is None else delta.dtype
     _call("veda_add_rms_norm", dev, stream, shape[0], shape[1], _type(x, "x"), xp, ldx,
@@ -516,6 +523,8 @@ def veda_add_rms_norm_fp8(x: torch.Tensor, delta: Optional[torch.Tensor], weight
     xp, ldx = _rows(x, "x", dev)
     dp, ldd = _rows(delta, "delta", dev, shape)
     rows, C = shape
+    if C >> 31:
+        _too_large(C)
     tx = _type(x, "x")
     _call("veda_add_rms_norm_fp8", dev, stream, rows, C, tx, xp, ldx,
           tx if delta is None else _type(delta, "delta"), dp, ldd, _at(weight, "weight", dev, _F32, (C,)), eps,
@@ -532,8 +541,8 @@ def _layer_norm_forward(x, delta, weight, eps, h, y, scale) -> None:
     dev = x.get_device()
     rows, C = x.shape
     tx = _DTYPES.get(x.dtype)
-    if dev < 0 or tx is None:
-        _device(x, "x"), _type(x, "x")
+    if dev < 0 or tx is None or C >> 31:
+        _device(x, "x"), _type(x, "x"), _too_large(C)
     if delta is None:
         td, dp, ldd = tx, None, 0
     else:
@@ -568,6 +577,8 @@ def _layer_gemm(a, a_scale, b, b_scale, bias, out_dtype) -> torch.Tensor:
     (M, K), (N, Kb) = a.shape, b.shape
     if a.dtype is not FP8 or b.dtype is not FP8 or Kb != K:
         raise ValueError(f"a and b must be {FP8} [M, K] and [N, K] (got {a.dtype} {tuple(a.shape)}, {b.dtype} {tuple(b.shape)})")
+    if (M | N | K) >> 31:
+        _too_large(M, N, K)
     kb = (K + 127) // 128
     out = a.new_empty((M, N), dtype=out_dtype)
     _call("veda_gemm_fp8", dev, None, M, N, K, ap, lda, _at(a_scale, "a_scale", dev, _F32, (kb, M)), bp, ldb,
@@ -578,6 +589,8 @@ def _layer_gemm(a, a_scale, b, b_scale, bias, out_dtype) -> torch.Tensor:
 
 def veda_add_rms_norm_backward_workspace(rows: int, C: int, device=None) -> int:
     n = _SZ()
+    if C >> 31:
+        _too_large(C)
     if device is not None and device != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
             return veda_add_rms_norm_backward_workspace(rows, C)
@@ -593,6 +606,8 @@ def veda_add_rms_norm_backward(h: torch.Tensor, dy: torch.Tensor, dh: Optional[t
     dev, shape = _device(h, "h"), h.shape
     if len(shape) != 2:
         raise ValueError("h must be [rows, C]")
+    if shape[1] >> 31:
+        _too_large(shape[1])
     th, td = h.dtype, dy.dtype
     _call("veda_add_rms_norm_backward", dev, stream, shape[0], shape[1], _type(h, "h"), _at(h, "h", dev, th, shape),
           _type(dy, "dy"), _at(dy, "dy", dev, td, shape), _at(dh, "dh", dev, th, shape),
@@ -620,6 +635,8 @@ def veda_quant_fp8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, stream
         raise ValueError("x must be [rows, C] or [B, heads, N, d]")
     if d > 1 and sd != 1:
         raise ValueError("the channels of x must be contiguous")
+    if (B | heads | d) >> 31:
+        _too_large(B, heads, d)
     rows, C = B * N, heads * d
     _call("veda_quant_fp8", dev, stream, B, N, heads, d, _type(x, "x"), x.data_ptr(),
           sb if B > 1 else 0, sn if N > 1 else 0, sh if heads > 1 else 0,
@@ -633,6 +650,8 @@ def veda_quant_fp8_weight(w: torch.Tensor, q: torch.Tensor, scale: torch.Tensor,
     if w.dim() != 2:
         raise ValueError("w must be [N, K]")
     N, K = w.shape
+    if (N | K) >> 31:
+        _too_large(N, K)
     _call("veda_quant_fp8_weight", dev, stream, N, K, _type(w, "w"), _at(w, "w", dev, w.dtype, (N, K)),
           _at(q, "q", dev, FP8, (N, K)), _at(scale, "scale", dev, _F32, ((N + 127) // 128, (K + 127) // 128)))
     return q
@@ -650,6 +669,8 @@ def veda_gemm_fp8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_sca
         raise ValueError(f"a and b must be {FP8} (got {a.dtype} and {b.dtype})")
     if b.shape[1] != K:
         raise ValueError(f"b must be [N, {K}] (got {tuple(b.shape)})")
+    if (M | N | K) >> 31:
+        _too_large(M, N, K)
     op, ldo = _rows(out, "out", dev, (M, N))
     kb = (K + 127) // 128
     _call("veda_gemm_fp8", dev, stream, M, N, K, ap, lda, _at(a_scale, "a_scale", dev, _F32, (kb, M)), bp, ldb,
@@ -664,6 +685,8 @@ def veda_rope_table(table: torch.Tensor, theta: float = 10000.0, start: float = 
     dev = _device(table, "table")
     if table.dim() != 3 or table.shape[2] != 2:
         raise ValueError("table must be [n, dim/2, 2]")
+    if (table.shape[0] | 2 * table.shape[1]) >> 31:
+        _too_large(*table.shape)
     _call("veda_rope_table", dev, stream, table.shape[0], 2 * table.shape[1], theta, start, step,
           _at(table, "table", dev, _F32, table.shape))
     return table
@@ -690,7 +713,10 @@ def make_rope(B: int, heads: int, d: int, grid: Sequence[int], tables: Sequence[
             raise ValueError(f"a table must be [at least {n}, pairs, 2] (got {tuple(shape)})")
         dims.append(2 * shape[1])
         ptrs.append(_at(t, "a table", _device(t, "a table"), _F32, shape) if shape[1] else None)
-    return veda_rope(B, heads, d, veda_grid(*map(int, grid)), *dims, *ptrs, _PAIRINGS[pairing], _NORMS[norm], eps)
+    T, H, W = map(int, grid)
+    if max(B, heads, d, T, H, W, *dims) >> 31:
+        _too_large(B, heads, d, T, H, W, *dims)
+    return veda_rope(B, heads, d, veda_grid(T, H, W), *dims, *ptrs, _PAIRINGS[pairing], _NORMS[norm], eps)
 
 
 def _tokens(t: Optional[torch.Tensor], r: veda_rope, name: str, dev: int, dtype: torch.dtype, shape):

@@ -45,12 +45,11 @@ def _flat(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
         return None
     if t.dim() != 2:
         t = t.reshape(t.numel() // t.shape[-1] if t.dim() and t.shape[-1] else 0, t.shape[-1] if t.dim() else 0)
-    aligned = t.data_ptr() % 16 == 0
     if t.is_contiguous():
-        return t if aligned else t.clone()
+        return t.clone() if t.data_ptr() & 15 else t
     rows, C = t.shape
     stride, step = t.stride()
-    fits = aligned and (step == 1 or C == 1) and (rows == 1 or (stride >= C and stride % 8 == 0))
+    fits = t.data_ptr() % 16 == 0 and (step == 1 or C == 1) and (rows == 1 or (stride >= C and stride % 8 == 0))
     return t if fits else t.contiguous()
 
 
