@@ -289,3 +289,20 @@ def test_sizes_past_32_bits_are_refused(V, monkeypatch):
             call()
             raise AssertionError(f"call {i} was made")
     assert made == []
+
+
+def test_inputs_whose_gradient_would_be_lost_are_refused(V):
+    """Tables and 8-bit operands that want a gradient: there is none, and the call says so."""
+    qkv = torch.zeros(1, 24, 3, 2, 64, dtype=torch.bfloat16)
+    tables = tuple(torch.zeros(n, dim, 2) for n, dim in zip((2, 3, 4), (12, 10, 10)))
+    tables[1].requires_grad_()
+    with pytest.raises(ValueError, match="no gradient"):
+        V.qkv_norm_rope(qkv, (2, 3, 4), tables, norm="none")
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA tensor"):
+        V.qkv_norm_rope(qkv, (2, 3, 4), tables, norm="none")
+    a, s = torch.zeros(4, 64, dtype=torch.float8_e4m3fn), torch.ones(1, 4)
+    for i in (0, 2):
+        args = [a, s, a, s]
+        args[i] = a.clone().requires_grad_()
+        with pytest.raises(ValueError, match="no gradient"):
+            V.gemm_fp8(*args)

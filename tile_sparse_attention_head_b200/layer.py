@@ -198,7 +198,7 @@ def gemm_fp8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: t
              bias: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
              out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """[M, N] = a [M, K] @ b [N, K]^T (+ bias fp32 [N]) of e4m3 operands with a scale for each block of 128."""
-    _no_grad_inputs("gemm_fp8", a_scale, b_scale, bias)
+    _no_grad_inputs("gemm_fp8", a, a_scale, b, b_scale, bias)
     if out is None:
         return B._layer_gemm(a, a_scale, b, b_scale, bias, out_dtype)
     return B.veda_gemm_fp8(a, a_scale, b, b_scale, bias, out)
@@ -287,7 +287,8 @@ def qkv_norm_rope(qkv, grid: Sequence[int], tables: Sequence[Optional[torch.Tens
     a table from a later row on moves the grid along that axis.  norm: RMS norm
     of q and k over all channels of a token ("row", weights [heads*d] fp32), over
     each head ("head", weights [d]) or "none".  pairing: "interleaved" or
-    "halves" of each axis's channels.  Differentiable in qkv, wq and wk."""
+    "halves" of each axis's channels.  Differentiable in qkv, wq and wk; tables
+    that want a gradient are refused."""
     if isinstance(qkv, torch.Tensor):
         if qkv.dim() != 5 or qkv.shape[2] != 3:
             raise ValueError(f"qkv must be [B, N, 3, heads, d] (got {tuple(qkv.shape)})")
@@ -307,6 +308,8 @@ def qkv_norm_rope(qkv, grid: Sequence[int], tables: Sequence[Optional[torch.Tens
     for t in tables:
         if t is not None and t.get_device() != xs[0].get_device():
             raise ValueError(f"a table is on {t.device}, qkv on {xs[0].device}")
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise ValueError("the tables have no gradient (detach them, or call it under torch.no_grad())")
     rope = B.make_rope(b, heads, d, grid, tables, pairing, norm, eps)
     if _wants_grad(wq, wk, *xs):
         return _QkvNormRope.apply(rope, tuple(tables), (tuple(grid), pairing, norm, eps), wq, wk, *xs)
