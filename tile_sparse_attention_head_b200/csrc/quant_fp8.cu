@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const __grid_constant__
     for (int off = 8; off; off >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, off));
     if (here && VEDA_IN_BOUNDS(row < A.rows && c + 8 <= A.C)) {
       *reinterpret_cast<uint2*>(A.q + (long long)row * A.C + c) = to_e4m3(v, e4m3_factor(a));
-      if (l == 0) A.scale[kb * A.rows + row] = e4m3_scale(a);
+      if (l == 0 && VEDA_IN_BOUNDS(kb < blocks)) A.scale[kb * A.rows + row] = e4m3_scale(a);
     }
   }
 }
@@ -84,10 +84,10 @@ __global__ void __launch_bounds__(256) quant_weight_kernel(const T* __restrict__
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int n = n0 + 16 * i;
-    if (n < N && c < K && VEDA_IN_BOUNDS(c + 8 <= K))
+    if (n < N && c < K && VEDA_IN_BOUNDS(n < N && c + 8 <= K))
       *reinterpret_cast<uint2*>(q + (long long)n * K + c) = to_e4m3(v[i], f);
   }
-  if (threadIdx.x == 0) scale[blockIdx.x] = e4m3_scale(a);
+  if (threadIdx.x == 0 && VEDA_IN_BOUNDS(nb < (N + 127) / 128 && kb < kbs)) scale[blockIdx.x] = e4m3_scale(a);
 }
 
 cudaError_t launch_quant_rows(QuantArgs a, int type, cudaStream_t s) {

@@ -94,7 +94,8 @@ __global__ void __launch_bounds__(512) add_rms_norm_kernel(const __grid_constant
     for (int i = 0; i < CPT; ++i) {
       to_pairs(hw[i], v[i]);
       if (g.t + i * g.tpt < nchunk) {
-        if (has_h && VEDA_IN_BOUNDS(row < A.rows)) store_words(h + 8 * i * g.tpt, hw[i], A.wide);
+        if (has_h && VEDA_IN_BOUNDS(row < A.rows && 8 * (g.t + i * g.tpt) + 8 <= A.C))
+          store_words(h + 8 * i * g.tpt, hw[i], A.wide);
 #pragma unroll
         for (int k = 0; k < 4; ++k) ss = f2_fma(v[i][k], v[i][k], ss);
       }
@@ -112,12 +113,14 @@ __global__ void __launch_bounds__(512) add_rms_norm_kernel(const __grid_constant
         if (in) a = max_abs(a, v[i]);
 #pragma unroll
         for (int off = 8; off; off >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, off));
-        if (in) {
+        if (in && VEDA_IN_BOUNDS(row < A.rows && 8 * (g.t + i * g.tpt) + 8 <= A.C)) {
           *reinterpret_cast<uint2*>(y + 8 * i * g.tpt) = to_e4m3(v[i], e4m3_factor(a));
-          if ((g.lane & 15) == 0) scale[2 * g.W * i * A.rows + row] = e4m3_scale(a);
+          if ((g.lane & 15) == 0 && VEDA_IN_BOUNDS((g.t >> 4) + 2 * g.W * i < (A.C + 127) / 128))
+            scale[2 * g.W * i * A.rows + row] = e4m3_scale(a);
         }
       } else {
-        if (in) store_pairs(y + 8 * i * g.tpt, v[i], A.wide);
+        if (in && VEDA_IN_BOUNDS(row < A.rows && 8 * (g.t + i * g.tpt) + 8 <= A.C))
+          store_pairs(y + 8 * i * g.tpt, v[i], A.wide);
       }
     }
     h += step * A.C;
@@ -199,7 +202,7 @@ __global__ void __launch_bounds__(512) add_rms_norm_bwd_kernel(const __grid_cons
           acc[i][k] = f2_fma(f2_mul(gv[i][k], rr), hv[i][k], acc[i][k]);
           d[k] = f2_fma(rr, f2_fma(hv[i][k], cc, f2_mul(gv[i][k], w[i][k])), d[k]);
         }
-        if (VEDA_IN_BOUNDS(row < A.rows)) {
+        if (VEDA_IN_BOUNDS(row < A.rows && here == row * A.C + 8 * g.t && 8 * (g.t + i * g.tpt) + 8 <= A.C)) {
           if (has_dx) store_pairs(static_cast<TX*>(A.dx) + here + 8 * i * g.tpt, d, A.wide);
           if (has_dd) store_pairs(static_cast<TD*>(A.ddelta) + here + 8 * i * g.tpt, d, A.wide);
         }
