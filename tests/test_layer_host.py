@@ -306,3 +306,47 @@ def test_inputs_whose_gradient_would_be_lost_are_refused(V):
         args[i] = a.clone().requires_grad_()
         with pytest.raises(ValueError, match="no gradient"):
             V.gemm_fp8(*args)
+
+
+def test_rotary_tables_of_another_device_are_refused(V, monkeypatch):
+    """The C struct holds addresses only: make_rope takes tables of one device, and the calls take operands of that
+    device.  The struct keeps its tables alive."""
+    import gc
+    import weakref
+    B = V.binding
+
+    class On:
+        """A tensor as of a device of its own."""
+
+        def __init__(self, t, dev):
+            self.t, self.dev, self.is_cuda, self.device = t, dev, True, f"cuda:{dev}"
+
+        def get_device(self):
+            return self.dev
+
+        def __getattr__(self, name):
+            return getattr(self.t, name)
+
+    def tables(*devs):
+        return tuple(On(torch.zeros(n, dim, 2), d) for n, dim, d in zip((2, 3, 4), (12, 10, 10), devs))
+
+    with pytest.raises(ValueError, match="cuda:1"):
+        V.make_rope(1, 2, 64, (2, 3, 4), tables(0, 0, 1), norm="none")
+    made = []
+    monkeypatch.setattr(B, "_call", lambda *a: made.append(a[0]))
+    t = tables(0, 0, 0)
+    r, ref = V.make_rope(1, 2, 64, (2, 3, 4), t, norm="none"), weakref.ref(t[1])
+    del t
+    gc.collect()
+    assert ref() is not None
+    x, o = (torch.zeros(s, dtype=torch.bfloat16) for s in ((1, 24, 2, 64), (1, 2, 24, 64)))
+    with pytest.raises(ValueError, match="tables are on cuda:0"):
+        V.veda_qkv_norm_rope(r, On(x, 1), None, None, None, None, On(o, 1), None, None)
+    with pytest.raises(ValueError, match="tables are on cuda:0"):
+        V.veda_qkv_norm_rope_backward(r, None, None, None, None, On(o, 1), None, None, On(x, 1), None, None, None, None, None)
+    assert made == []
+    V.veda_qkv_norm_rope(r, On(x, 0), None, None, None, None, On(o, 0), None, None)
+    assert made == ["veda_qkv_norm_rope"]
+    del r
+    gc.collect()
+    assert ref() is None

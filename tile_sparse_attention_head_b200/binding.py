@@ -55,6 +55,7 @@ class veda_mlp_grad(ctypes.Structure):
 
 
 class veda_rope(ctypes.Structure):
+    tables, device = (), None     # make_rope: what the pointers point into, and where that is
     _fields_ = [("B", ctypes.c_int32), ("heads", ctypes.c_int32), ("d", ctypes.c_int32), ("grid", veda_grid),
                 ("dim_t", ctypes.c_int32), ("dim_h", ctypes.c_int32), ("dim_w", ctypes.c_int32),
                 ("table_t", ctypes.c_void_p), ("table_h", ctypes.c_void_p), ("table_w", ctypes.c_void_p),
@@ -695,14 +696,14 @@ def veda_rope_table(table: torch.Tensor, theta: float = 10000.0, start: float = 
 def make_rope(B: int, heads: int, d: int, grid: Sequence[int], tables: Sequence[Optional[torch.Tensor]],
               pairing: str = "interleaved", norm: str = "row", eps: float = 1e-6) -> veda_rope:
     """C struct of a rotary description; tables (time, height, width): fp32 [at least the grid's size, pairs, 2]
-    device tensors, or None for an axis without channels.  The tensors must outlive the struct's use."""
+    device tensors of one device, or None for an axis without channels.  The struct keeps them alive."""
     if norm not in _NORMS:
         raise ValueError(f"norm must be one of {sorted(_NORMS)} (got {norm!r})")
     if pairing not in _PAIRINGS:
         raise ValueError(f"pairing must be one of {sorted(_PAIRINGS)} (got {pairing!r})")
     if len(grid) != 3 or len(tables) != 3:
         raise ValueError("grid and tables have three entries: time, height, width")
-    dims, ptrs = [], []
+    dims, ptrs, dev = [], [], None
     for t, n in zip(tables, grid):
         if t is None:
             dims.append(0)
@@ -712,11 +713,19 @@ def make_rope(B: int, heads: int, d: int, grid: Sequence[int], tables: Sequence[
         if len(shape) != 3 or shape[2] != 2 or shape[0] < n:
             raise ValueError(f"a table must be [at least {n}, pairs, 2] (got {tuple(shape)})")
         dims.append(2 * shape[1])
-        ptrs.append(_at(t, "a table", _device(t, "a table"), _F32, shape) if shape[1] else None)
+        dev = _device(t, "a table") if dev is None else dev
+        ptrs.append(_at(t, "a table", dev, _F32, shape) if shape[1] else None)
     T, H, W = map(int, grid)
     if max(B, heads, d, T, H, W, *dims) >> 31:
         _too_large(B, heads, d, T, H, W, *dims)
-    return veda_rope(B, heads, d, veda_grid(T, H, W), *dims, *ptrs, _PAIRINGS[pairing], _NORMS[norm], eps)
+    r = veda_rope(B, heads, d, veda_grid(T, H, W), *dims, *ptrs, _PAIRINGS[pairing], _NORMS[norm], eps)
+    r.tables, r.device = tables, dev
+    return r
+
+
+def _same_device(r: veda_rope, dev: int) -> None:
+    if r.device is not None and r.device != dev:
+        raise ValueError(f"the tables are on cuda:{r.device}, the operands on cuda:{dev}")
 
 
 def _tokens(t: Optional[torch.Tensor], r: veda_rope, name: str, dev: int, dtype: torch.dtype, shape):
@@ -751,6 +760,7 @@ def veda_qkv_norm_rope(r: veda_rope, q: Optional[torch.Tensor], k: Optional[torc
     if some is None:
         raise ValueError("one of q, k and v is needed")
     dev, dt, n = _device(some, "q, k, v"), some.dtype, r.grid.T * r.grid.H * r.grid.W
+    _same_device(r, dev)
     ins, outs = (r.B, n, r.heads, r.d), (r.B, r.heads, n, r.d)
     _call("veda_qkv_norm_rope", dev, stream, ctypes.byref(r), _type(some, "q, k, v"), _tokens(q, r, "q", dev, dt, ins),
           _tokens(k, r, "k", dev, dt, ins), _tokens(v, r, "v", dev, dt, ins), _norm_weight(wq, r, "wq", dev),
@@ -790,6 +800,7 @@ def veda_qkv_norm_rope_backward(r: veda_rope, q: Optional[torch.Tensor], k: Opti
     if some is None:
         raise ValueError("one of dq, dk and dv is needed")
     dev, dt, n, bf = _device(some, "dq, dk, dv"), some.dtype, r.grid.T * r.grid.H * r.grid.W, torch.bfloat16
+    _same_device(r, dev)
     ins, outs = (r.B, n, r.heads, r.d), (r.B, r.heads, n, r.d)
     _call("veda_qkv_norm_rope_backward", dev, stream, ctypes.byref(r), _type(some, "dq, dk, dv"),
           _tokens(q, r, "q", dev, dt, ins), _tokens(k, r, "k", dev, dt, ins), _norm_weight(wq, r, "wq", dev),
