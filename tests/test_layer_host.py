@@ -308,6 +308,13 @@ def test_inputs_whose_gradient_would_be_lost_are_refused(V):
             V.gemm_fp8(*args)
 
 
+@pytest.mark.parametrize("grid", [(2 - 2 ** 32, 3, 4), (2, 3 - 2 ** 32, 4), (-2, -3, 4), (0, 3, 4)])
+def test_grids_that_are_none_are_refused(V, grid):
+    """A negative size may be a valid one in its low 32 bits, for which the tables are too short."""
+    with pytest.raises(ValueError, match="grid dimensions"):
+        V.make_rope(1, 2, 64, grid, (None, None, None), norm="none")
+
+
 def test_rotary_tables_of_another_device_are_refused(V, monkeypatch):
     """The C struct holds addresses only: make_rope takes tables of one device, and the calls take operands of that
     device.  The struct keeps its tables alive."""

@@ -716,6 +716,8 @@ def make_rope(B: int, heads: int, d: int, grid: Sequence[int], tables: Sequence[
         dev = _device(t, "a table") if dev is None else dev
         ptrs.append(_at(t, "a table", dev, _F32, shape) if shape[1] else None)
     T, H, W = map(int, grid)
+    if min(T, H, W) < 1:      # also what would be a valid size in its low 32 bits
+        raise ValueError(f"grid dimensions must be >= 1 (got {T} x {H} x {W})")
     if max(B, heads, d, T, H, W, *dims) >> 31:
         _too_large(B, heads, d, T, H, W, *dims)
     r = veda_rope(B, heads, d, veda_grid(T, H, W), *dims, *ptrs, _PAIRINGS[pairing], _NORMS[norm], eps)
