@@ -21,14 +21,15 @@
 // their registers while the next block is multiplied.  Results leave through
 // shared memory and TMA stores, which drop what lies past M and N.
 //
-// Measured, 75,600 x 5,120 x 15,360: 6.0 to 6.8 ms in short runs, 7.1 ms in long
-// ones (1.98 to 1.67 PFLOP/s).  What bounds it is the power limit with normal data
-// (with zeros 5.1 ms; the multiplications and loads alone 4.8 and 3.6 ms), and
-// the adding warps' chain per block -- wait, load, add -- of about 1,040 cycles
-// at 512 of tensor work.  So the chain is kept short: a
-// stage's one barrier says that it is free, that its sums are there and that the
-// scales are, and the load of the next 32 columns, of the next block too, is
-// under way while 32 are added.
+// Measured, 75,600 x 5,120 x 15,360: 6.0 to 6.8 ms in short runs, 7.0 to 7.2 ms in
+// long ones (1.98 to 1.66 PFLOP/s).  What bounds it first is the adding warps'
+// chain per block -- wait, load, add: with zeros as data, which stay below the
+// power limit, 5.1 to 5.7 ms between boxes, 1,040 to 1,160 cycles a block at 512 of
+// tensor work.  With normal data the power limit comes on top (long runs are at
+// 1.6 GHz); the multiplications and loads alone took 4.8 ms, 3.6 with zeros.  So the
+// chain is kept short: a stage's one barrier says that it is free, that its sums
+// are there and that the scales are, and the load of the next 32 columns, of the
+// next block too, is under way while 32 are added.
 #include "layer_common.cuh"
 #include "kernels.h"
 #undef VEDA_SRC_ID
@@ -712,16 +713,20 @@ inline int gemm_bn(int M, int N, int sms) {
   return ((M + 255LL) / 256) * ((N + 127LL) / 128) * 2 <= sms ? 128 : 256;
 }
 
-// Chooses the kernel -- few = 0: 256 x bn tiles; otherwise the rows per tile of
+// Chooses the kernel -- few = 0: tiles of 256 x bn; otherwise the rows per tile of
 // the one for few rows -- and into how many CTAs a tile's k blocks are split.
-// Measured on 148 SMs, us at the better split, few rows / 256 x 256 tiles:
-//   M =    1: 17.3 / 32.0 (N, K = 15,360, 5,120), 10.5 / 25.3 (5,120, 5,120), 5.1 / 11.9 (1,536, 1,536)
-//   M =   64: 23.0 / 26.8, 14.1 / 25.6, 7.0 / 12.4
-//   M =  128: 33.1 / 27.4, 20.7 / 26.1, 8.4 / 12.7     64-row tiles: 240, 80, 24
-//   M =  256: 62.4 / 28.2, 31.8 / 26.2, 9.8 / 12.7                   480, 160, 48
-//   M =  512:              54.3 / 26.4, 13.3 / 12.7                       320, 96
+// Measured on 148 SMs with weights that are not in L2, us, few rows at the better
+// split / tiles (256 x 128 where these fit in one go):
+//   N, K =   15,360, 5,120   5,120, 5,120   4,608, 1,536   1,536, 1,536
+//   M =   1:   18.7 / 36.8    10.7 / 25.8     6.7 / 11.7     4.9 / 11.0
+//   M =  64:   23.8 / 32.2    14.3 / 23.7    10.1 / 11.7     7.1 / 11.4
+//   M = 128:   33.9 / 32.6    20.6 / 24.1    11.3 / 12.1     8.4 / 11.9    64-row tiles: 240, 80, 72, 24
+//   M = 192:   59.4 / 33.3    21.4 / 24.0    13.2 / 12.1     9.8 / 11.9                  360, 120, 108, 36
+//   M = 256:   62.3 / 33.6    31.3 / 24.3    13.5 / 12.2     9.9 / 11.8                  480, 160, 144, 48
+//   M = 512:    116 / 58.8    52.5 / 29.4    16.9 / 12.5    11.9 / 11.9                  960, 320, 288, 96
 // So up to 64 rows, and with more while 64-row tiles fill at most 5/9 of the
-// SMs.  Splits are worth it up to 5/3 CTAs per SM.
+// SMs (82 of them); above that the better one depends on K, by 12% at most (120
+// and 108 tiles above).  Splits are worth it up to 5/3 CTAs per SM.
 void plan_gemm_fp8(GemmArgs* a, int sms) {
   a->few = 0;
   a->split = 1;

@@ -147,7 +147,8 @@ cudaError_t launch_attn_bwd_dkdv(const Geometry& G, const BwdMaps<kMaxGridMaps>&
 
 unsigned long long current_context_id();   // veda_api.cu
 
-// n / d for 0 <= n < 2^31 by one multiplication.
+// n / d for 0 <= n < 2^31 by one high multiplication with a rounded-up reciprocal
+// (Granlund and Montgomery, "Division by invariant integers using multiplication").
 struct FastDiv {
   uint32_t d, mul, shift;
   FastDiv() = default;

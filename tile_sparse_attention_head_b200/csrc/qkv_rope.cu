@@ -27,11 +27,14 @@
 //
 // Measured (6,548 GB/s is the rate of a plain copy): 75,600 tokens of 40 x 128
 // 930 us, 5.0 TB/s; 32,760 tokens of 12 x 128 forward 127 us (4.8 TB/s), backward
-// 215 us (3.5 TB/s).  Issue slots bound it now, 16 instructions a channel forward
-// and 31 backward at 60% issue: a row costs a thread some 190 instructions
-// whatever its chunks (sums across the group, angles, addresses).  Walking
-// consecutive tokens with additions instead of divisions took more of them, and
-// more warps per SM spill.
+// 215 to 221 us (3.5 TB/s).  With halves, whose eight angle places spill above one
+// chunk a thread, 1,690, 210 and 325 us.  fp16 input takes what bf16 does, fp32 160
+// us forward and 264 us backward.  What bounds it now is latency at 16 to 20 warps an
+// SM: 16 instructions a channel forward and 31 backward fill 60% of the issue
+// slots, and the warps wait for their own last instruction or for shared memory.
+// A row costs a thread some 190 instructions whatever its chunks (sums across
+// the group, angles, addresses).  Walking consecutive tokens with additions
+// instead of divisions took more of them, and more warps per SM spill.
 #include "layer_common.cuh"
 #include "kernels.h"
 #undef VEDA_SRC_ID

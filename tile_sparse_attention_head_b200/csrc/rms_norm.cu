@@ -19,8 +19,8 @@
 // in flight through the reduction's barrier and the stores.
 //
 // Measured (6,548 GB/s is the rate of a plain copy): 75,600 x 5,120 bf16 with
-// e4m3 output 438 us, 6.2 TB/s; 32,760 x 1,536, fp32 stream beside bf16: forward
-// 94 us (5.9 TB/s), backward 119 us (6.4 TB/s).  Before the arithmetic ran on
+// e4m3 output 440 to 500 us between boxes (6.2 to 5.4 TB/s); 32,760 x 1,536, fp32
+// stream beside bf16: forward 94 us (5.9 TB/s), backward 119 us (6.4 TB/s).  Before the arithmetic ran on
 // pairs the 8-bit form was bound by issue slots (37 instructions a channel, now
 // 21, half of them a row's fixed part).
 //
