@@ -721,7 +721,7 @@ def make_rope(B: int, heads: int, d: int, grid: Sequence[int], tables: Sequence[
     if max(B, heads, d, T, H, W, *dims) >> 31:
         _too_large(B, heads, d, T, H, W, *dims)
     r = veda_rope(B, heads, d, veda_grid(T, H, W), *dims, *ptrs, _PAIRINGS[pairing], _NORMS[norm], eps)
-    r.tables, r.device = tables, dev
+    r.tables, r.device = tuple(tables), dev
     return r
 
 

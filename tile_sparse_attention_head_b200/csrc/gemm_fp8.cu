@@ -24,7 +24,7 @@
 // Measured, 75,600 x 5,120 x 15,360: 6.0 to 6.8 ms in short runs, 7.0 to 7.2 ms in
 // long ones (1.98 to 1.66 PFLOP/s).  What bounds it first is the adding warps'
 // chain per block -- wait, load, add: with zeros as data, which stay below the
-// power limit, 5.1 to 5.7 ms between boxes, 1,040 to 1,160 cycles a block at 512 of
+// power limit, 5.1 to 5.7 ms between GPUs, 1,040 to 1,160 cycles a block at 512 of
 // tensor work.  With normal data the power limit comes on top (long runs are at
 // 1.6 GHz); the multiplications and loads alone took 4.8 ms, 3.6 with zeros.  So the
 // chain is kept short: a stage's one barrier says that it is free, that its sums

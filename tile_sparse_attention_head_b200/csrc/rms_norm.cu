@@ -19,10 +19,10 @@
 // in flight through the reduction's barrier and the stores.
 //
 // Measured (6,548 GB/s is the rate of a plain copy): 75,600 x 5,120 bf16 with
-// e4m3 output 440 to 500 us between boxes (6.2 to 5.4 TB/s); 32,760 x 1,536, fp32
-// stream beside bf16: forward 94 us (5.9 TB/s), backward 119 us (6.4 TB/s).  Before the arithmetic ran on
-// pairs the 8-bit form was bound by issue slots (37 instructions a channel, now
-// 22, half of them a row's fixed part).
+// e4m3 output 440 to 500 us between GPUs (6.2 to 5.4 TB/s); 32,760 x 1,536, fp32
+// stream beside bf16: forward 94 us (5.9 TB/s), backward 119 to 127 us (6.4 to 6.0
+// TB/s).  Before the arithmetic ran on pairs the 8-bit form was bound by issue
+// slots (37 instructions a channel, now 22, half of them a row's fixed part).
 //
 // dw: each group sums its own rows in registers, a CTA adds its groups in shared
 // memory and writes one partial row, and a second kernel adds the partial rows,
